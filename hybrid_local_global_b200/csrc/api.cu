@@ -291,6 +291,9 @@ namespace hlg {
 // Sets the message gemma_last_error() returns on this thread; for entry
 // points defined in other translation units of the library.
 int record_error(int code, const char* msg) { return fail(code, "%s", msg); }
+int record_ok() { return succeed(); }
+int* device_status() { return status_ptr(); }
+int multiprocessors() { return sm_count(); }
 }  // namespace hlg
 
 extern "C" {
@@ -1058,6 +1061,174 @@ int gemma_attn_decode_multi_paged(const void* q, const void* k_new, const void* 
   return multi_impl(q, k_new, v_new, k_pool, v_pool, pages_per_seq * page_size, seq_lens, max_seq_len, batch, tokens,
                     0, n_q_heads, n_kv_heads, head_dim, rope_frac, rope_theta, scale, out, workspace,
                     workspace_bytes, flags, stream, CacheLayout{page_table, page_size, pages_per_seq, n_pages});
+}
+
+// Window plus sinks on a paged cache: checks shared by prefill and decode. On
+// success *v_pool_io is the pool the values are read from.
+static int check_sinks(const void* q, const void* k_new, const void* v_new, void* k_pool, void** v_pool_io,
+                       const int32_t* page_table, int page_size, int pages_per_seq, int n_pages, int batch, int window,
+                       int sinks, int n_q_heads, int n_kv_heads, int head_dim, float rope_frac, float rope_theta,
+                       float scale, const void* out, unsigned flags) {
+  int rc = check_paged(page_table, page_size, pages_per_seq, n_pages);
+  if (rc) return rc;
+  rc = check_heads(n_q_heads, n_kv_heads, head_dim, 0, rope_frac, rope_theta, scale);
+  if (rc) return rc;
+  if (window <= 0) return fail(GEMMA_ERR_INVALID_ARG, "window %d must be positive", window);
+  if (sinks < 0) return fail(GEMMA_ERR_INVALID_ARG, "sinks %d must not be negative", sinks);
+  if (flags & GEMMA_F_SOURCE_WINDOW)
+    return fail(GEMMA_ERR_INVALID_ARG, "GEMMA_F_SOURCE_WINDOW: a paged cache keeps the rows its sharers read");
+  rc = check_kv_flags(flags, 0, k_new, v_new, k_pool, v_pool_io);
+  if (rc) return rc;
+  if (flags & GEMMA_F_KV_INT8)
+    return fail(GEMMA_ERR_UNSUPPORTED, "GEMMA_F_KV_INT8: window-plus-sinks attention takes bf16 pools");
+  if (batch <= 0 || batch > 65535) return fail(GEMMA_ERR_INVALID_ARG, "batch %d (1 to 65535)", batch);
+  if (n_kv_heads > 65535) return fail(GEMMA_ERR_UNSUPPORTED, "n_kv_heads %d > 65535", n_kv_heads);
+  if (!q || !out || !k_pool || !*v_pool_io) return fail(GEMMA_ERR_INVALID_ARG, "null tensor pointer");
+  if (!aligned16(q) || !aligned16(out) || !aligned16(k_pool) || !aligned16(*v_pool_io) ||
+      (k_new && !aligned16(k_new)) || (v_new && !aligned16(v_new)))
+    return fail(GEMMA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  return GEMMA_OK;
+}
+
+int gemma_attn_prefill_sinks(const void* q, const void* k_new, const void* v_new, void* k_pool, void* v_pool,
+                             const int32_t* page_table, int page_size, int pages_per_seq, int n_pages,
+                             const int32_t* seq_lens_before, int batch, int s_new, int window, int sinks,
+                             int n_q_heads, int n_kv_heads, int head_dim, float rope_frac, float rope_theta,
+                             float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                             unsigned flags, void* stream) {
+  if (s_new < 0) return fail(GEMMA_ERR_INVALID_ARG, "s_new %d", s_new);
+  if (s_new == 0) return succeed();  // empty tensors have no pointers to check
+  int rc = check_sinks(q, k_new, v_new, k_pool, &v_pool, page_table, page_size, pages_per_seq, n_pages, batch, window,
+                       sinks, n_q_heads, n_kv_heads, head_dim, rope_frac, rope_theta, scale, out, flags);
+  if (rc) return rc;
+  const int cache_cap = pages_per_seq * page_size;
+  if (cache_cap < s_new) return fail(GEMMA_ERR_CAPACITY, "cache capacity %d < s_new %d", cache_cap, s_new);
+  size_t off_k;
+  const size_t need = prefill_ws_parts(batch, s_new, n_q_heads, n_kv_heads, head_dim, 0, &off_k);
+  if (!workspace || workspace_bytes < need)
+    return fail(GEMMA_ERR_CAPACITY, "workspace %zu bytes < %zu", workspace_bytes, need);
+  if (!aligned16(workspace)) return fail(GEMMA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
+  int* status = status_ptr();
+  if (!status) return fail(GEMMA_ERR_CUDA, "no CUDA device");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+
+  // rotate, and write the chunk's rows at their positions, as a global layer
+  PrefillRopeArgs ra{};
+  ra.q = static_cast<const bf16*>(q);
+  ra.k_new = static_cast<const bf16*>(k_new);
+  ra.v_new = static_cast<const bf16*>(v_new);
+  ra.q_rot = static_cast<bf16*>(workspace);
+  ra.k_cache = static_cast<bf16*>(k_pool);
+  ra.v_cache = static_cast<bf16*>(v_pool);
+  ra.cache_cap = cache_cap;
+  ra.seq_lens_before = seq_lens_before;
+  ra.S = s_new;
+  ra.Hq = n_q_heads;
+  ra.Hkv = n_kv_heads;
+  ra.n_rot = rope_rotated_pairs(head_dim, rope_frac);
+  ra.log2_theta = std::log2((double)rope_theta);
+  ra.q_scale = (float)((double)scale * 1.4426950408889634);
+  ra.page_table = page_table;
+  ra.page_size = page_size;
+  ra.pages_per_seq = pages_per_seq;
+  ra.n_pages = n_pages;
+  ra.status = status;
+  cudaError_t e;
+  {
+    ProfScope p_rope(GEMMA_KERNEL_PREFILL_ROPE, st);
+    e = launch_prefill_rope(ra, batch, head_dim, st);
+    p_rope.done();
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "prefill rope launch");
+
+  const int64_t D = head_dim, ps = page_size;
+  PrefillAttnArgs aa{};
+  aa.q_rot = ra.q_rot;
+  aa.k = KVView{static_cast<const bf16*>(k_pool), (int64_t)n_kv_heads * ps * D, D, ps * D};
+  aa.v = KVView{static_cast<const bf16*>(v_pool), aa.k.stride_b, aa.k.stride_row, aa.k.stride_h};
+  aa.key_cap = cache_cap;
+  aa.seq_lens_before = seq_lens_before;
+  aa.S = s_new;
+  aa.window = window;
+  aa.sinks = sinks;
+  aa.Hq = n_q_heads;
+  aa.Hkv = n_kv_heads;
+  aa.scale_log2 = 1.0f;  // already applied to the rotated queries
+  aa.out = static_cast<bf16*>(out);
+  aa.lse = lse;
+  aa.status = status;
+  aa.wait_ns = (unsigned long long)g_wait_ns.load();
+  aa.page_table = page_table;
+  aa.page_size = page_size;
+  aa.pages_per_seq = pages_per_seq;
+  aa.n_pages = n_pages;
+  // head_dim 512 with an even number of q heads per KV head: head pairs, as
+  // in gemma_attn_prefill
+  const bool pair = head_dim == 512 && (n_q_heads / n_kv_heads) % 2 == 0;
+  {
+    ProfScope p_attn(GEMMA_KERNEL_PREFILL_ATTN, st);
+    e = pair ? launch_prefill_attn_pair(aa, batch, head_dim, page_size, 0, 1, st)
+             : launch_prefill_attn_tc(aa, batch, head_dim, page_size, 0, st);
+    p_attn.done();
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "prefill attention launch");
+  return succeed();
+}
+
+size_t gemma_attn_decode_sinks_workspace_size(int batch, int n_q_heads, int n_kv_heads, int head_dim, int window,
+                                              int sinks, int max_seq_len) {
+  (void)batch; (void)n_q_heads; (void)n_kv_heads; (void)head_dim; (void)window; (void)sinks; (void)max_seq_len;
+  return 0;
+}
+
+int gemma_attn_decode_sinks(const void* q, const void* k_new, const void* v_new, void* k_pool, void* v_pool,
+                            const int32_t* page_table, int page_size, int pages_per_seq, int n_pages,
+                            const int32_t* seq_lens, int max_seq_len, int batch, int window, int sinks,
+                            int n_q_heads, int n_kv_heads, int head_dim, float rope_frac, float rope_theta,
+                            float scale, void* out, void* workspace, size_t workspace_bytes, unsigned flags,
+                            void* stream) {
+  int rc = check_sinks(q, k_new, v_new, k_pool, &v_pool, page_table, page_size, pages_per_seq, n_pages, batch, window,
+                       sinks, n_q_heads, n_kv_heads, head_dim, rope_frac, rope_theta, scale, out, flags);
+  if (rc) return rc;
+  if (!seq_lens) return fail(GEMMA_ERR_INVALID_ARG, "null seq_lens");
+  if (max_seq_len <= 0) return fail(GEMMA_ERR_INVALID_ARG, "max_seq_len %d", max_seq_len);
+  if (pages_per_seq * page_size < max_seq_len)
+    return fail(GEMMA_ERR_CAPACITY, "cache capacity %d < max_seq_len %d", pages_per_seq * page_size, max_seq_len);
+  (void)workspace; (void)workspace_bytes;
+  int* status = status_ptr();
+  if (!status) return fail(GEMMA_ERR_CUDA, "no CUDA device");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  SinkDecodeArgs a{};
+  a.q = static_cast<const bf16*>(q);
+  a.k_new = static_cast<const bf16*>(k_new);
+  a.v_new = static_cast<const bf16*>(v_new);
+  a.k_pool = static_cast<bf16*>(k_pool);
+  a.v_pool = static_cast<bf16*>(v_pool);
+  a.page_table = page_table;
+  a.page_size = page_size;
+  a.pages_per_seq = pages_per_seq;
+  a.n_pages = n_pages;
+  a.seq_lens = seq_lens;
+  a.max_len = max_seq_len;
+  a.window = window;
+  a.sinks = sinks;
+  a.Hq = n_q_heads;
+  a.Hkv = n_kv_heads;
+  a.keqv = (flags & GEMMA_F_KEQV) ? 1 : 0;
+  a.n_rot = rope_rotated_pairs(head_dim, rope_frac);
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.out = static_cast<bf16*>(out);
+  a.status = status;
+  a.wait_ns = (unsigned long long)g_wait_ns.load();
+  a.drop_first_copy = g_drop_next.exchange(0);
+  cudaError_t e;
+  {
+    ProfScope p_split(GEMMA_KERNEL_DECODE_SPLIT, st);
+    e = launch_decode_sinks(a, batch, head_dim, std::log2((double)rope_theta), st);
+    p_split.done();
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "decode attention launch");
+  return succeed();
 }
 
 int gemma_attn_visible_ranges(const int32_t* seq_lens_before, int batch, int s_new, int window,

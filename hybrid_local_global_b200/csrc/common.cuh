@@ -28,6 +28,36 @@ __host__ __device__ __forceinline__ int64_t visible_range(int64_t pos, int windo
   return b >= a ? b - a + 1 : 0;
 }
 
+// Visible keys of a windowed query that also sees the sequence's first
+// `sinks` positions: the query at position len - 1 sees j < len iff
+// j >= lo (= len - window, at least 0) or j < sinks. They are walked in a
+// virtual order of whole 32-key blocks: n_sink keys from position 0, then from
+// position `start` on, n in all (the first and last block of a run may hold
+// positions that the query does not see).
+struct SinkSpan {
+  int lo, n_sink, start, n;
+  __host__ __device__ __forceinline__ int position(int v) const { return v < n_sink ? v : start + (v - n_sink); }
+  __host__ __device__ __forceinline__ bool sees(int pos, int len, int sinks) const {
+    return pos < len && (pos >= lo || pos < sinks);
+  }
+};
+
+__host__ __device__ __forceinline__ SinkSpan sink_span(int64_t len, int window, int sinks) {
+  SinkSpan s;
+  s.lo = len > window ? (int)(len - window) : 0;
+  s.n_sink = 0;
+  s.start = s.lo & ~31;
+  if (sinks > 0) {
+    const int first = sinks < s.lo ? (sinks + 31) & ~31 : s.lo;  // end of the sinks' blocks
+    if (first < s.start)
+      s.n_sink = first;
+    else
+      s.start = 0;  // the runs meet
+  }
+  s.n = s.n_sink + (int)(len - s.start);
+  return s;
+}
+
 // Cache addressing. A layer's cache is a pool of pages [n_pages][Hkv][ps][D];
 // position (or ring slot) p of sequence b lives at row p % ps of page
 // table[b * pps + p / ps]. A contiguous cache [B][Hkv][cap][D] is the case

@@ -99,6 +99,7 @@ struct PrefillAttnArgs {
                        // gathered for chunked local prefill); 0: view row = position
   const int32_t* seq_lens_before;  // device [B] or null
   int S, window, Hq, Hkv;
+  int sinks;           // > 0 (cache views, window > 0): positions below it stay visible
   float scale_log2;    // scale * log2(e)
   bf16* out;           // [B][S][Hq][D]
   float* lse;          // [B][Hq][S] or null
@@ -141,6 +142,12 @@ struct DecodeAttnArgs {
   const int32_t* page_table;
   int page_size, pages_per_seq, n_pages;
 };
+
+// Host state of the library (api.cu), for entry points defined elsewhere.
+int record_error(int code, const char* msg);  // sets gemma_last_error(), returns code
+int record_ok();                              // clears it, returns GEMMA_OK
+int* device_status();                         // the current device's status word, or null
+int multiprocessors();                        // of the current device
 
 cudaError_t launch_prefill_rope(const PrefillRopeArgs& a, int B, int D, cudaStream_t st);
 // Chunked local prefill: copies the ring's K/V of positions
@@ -215,6 +222,28 @@ cudaError_t launch_prefill_attn_tc(const PrefillAttnArgs& a, int B, int D, int k
 // tile (used when q heads per KV head is even) instead of two query tiles.
 cudaError_t launch_prefill_attn_pair(const PrefillAttnArgs& a, int B, int D, int key_rows_total,
                                      int kv_token_major, int head_pair, cudaStream_t st);
+// Single-token decode with window and sinks on a paged cache, one launch
+// (decode_sinks.cu): RoPE, append, attention, merge.
+struct SinkDecodeArgs {
+  const bf16* q;           // [B][Hq][D] pre-RoPE
+  const bf16* k_new;       // [B][Hkv][D] pre-RoPE, or null (shared layer)
+  const bf16* v_new;       // null under K = V
+  bf16* k_pool;            // [n_pages][Hkv][page_size][D]
+  bf16* v_pool;            // the key pool under K = V
+  const int32_t* page_table;
+  int page_size, pages_per_seq, n_pages;
+  const int32_t* seq_lens; // device [B], with the new token; 0: idle
+  int max_len, window, sinks, Hq, Hkv;
+  int keqv;
+  int n_rot;
+  float scale_log2;
+  bf16* out;               // [B][Hq][D]
+  int* status;
+  unsigned long long wait_ns;
+  int drop_first_copy;     // test hook: skip the first copy of the first work unit
+  double freq[256];        // half-turns per position of pair i (launch_decode_sinks fills it in)
+};
+cudaError_t launch_decode_sinks(SinkDecodeArgs& a, int B, int D, double log2_theta, cudaStream_t st);
 cudaError_t launch_decode_split(const DecodeAttnArgs& a, int B, int D, cudaStream_t st);
 // int8 cache: the same split-K decode reading codes and (min, step) rows
 cudaError_t launch_decode_split_q8(const DecodeAttnArgs& a, int B, int D, cudaStream_t st);

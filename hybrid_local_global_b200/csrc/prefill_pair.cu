@@ -98,6 +98,7 @@ struct PairCfg {
 
 struct PairArgs {
   int S, window, Hq, Hkv;
+  int sinks;  // SK instances: positions below it stay visible to every query
   int64_t key_cap;
   const int32_t* seq_lens_before;
   bf16* out;
@@ -173,7 +174,9 @@ __device__ __forceinline__ void clear_v_tail_pair(uint32_t stage, int r0) {
   asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
 }
 
-template <int D>
+// SK: a window plus sinks (cache views): the key tiles of the sinks, then the
+// tiles from the window's first one on.
+template <int D, bool SK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
     k_prefill_pair(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -212,7 +215,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
   visible_range(pos0 + pq0, a.window, n_keys, &lo_first, &hi_first);
   visible_range(pos0 + min(pq0 + span - 1, a.S - 1), a.window, n_keys, &lo_last, &hi_last);
   const int64_t kt0 = lo_first / BN;
-  const int n_tiles = (int)(hi_last / BN - kt0 + 1);
+  int n_tiles = (int)(hi_last / BN - kt0 + 1);
+  int n_st = 0;  // SK: tiles of the sinks, before tile kt0
+  if (SK) {
+    const int64_t sink_tiles = ((int64_t)a.sinks + BN - 1) / BN;
+    n_st = (int)(sink_tiles < kt0 ? sink_tiles : kt0);
+    n_tiles += n_st;
+  }
+  // first key of the j-th key tile
+  const auto tile_key = [&](int j) -> int64_t { return (SK && j < n_st ? j : kt0 + j - n_st) * BN; };
 
   if (threadIdx.x == 0) {
     mbar_init(&ctl->q_full, 1);
@@ -260,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
       for (int j = 0; j <= n_tiles && ok; ++j) {
         for (int kind = 0; kind < 2 && ok; ++kind) {  // 0: K_j, 1: V_{j-1}
           if ((kind == 0 && j == n_tiles) || (kind == 1 && j == 0)) continue;
-          int key0 = (int)((kt0 + j - kind) * BN - koff);  // view row
+          int key0 = (int)(tile_key(j - kind) - koff);  // view row
           int kb = b;                                           // view batch
           if (a.page_table) {
             // tiles never straddle a page (page_size is a multiple of 128); a
@@ -273,8 +284,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
             }
             key0 -= pi * a.page_size;
           }
-          const int n_st = kind == 0 ? Cfg::K_STAGES : 1;
-          for (int hs = 0; hs < n_st; ++hs, ++item) {
+          const int n_stg = kind == 0 ? Cfg::K_STAGES : 1;
+          for (int hs = 0; hs < n_stg; ++hs, ++item) {
             const int s = item % NSTAGE;
             if (item >= NSTAGE &&
                 !mbar_wait_bounded_at(&ctl->empty[s], ((item / NSTAGE) - 1) & 1, abort_flag, deadline,
@@ -356,7 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
           }
           ctl->consumed[s] += 1;
           const uint32_t st = sStage + s * STAGE_B;
-          const int64_t rows_valid = n_keys - (kt0 + j - 1) * BN;
+          const int64_t rows_valid = n_keys - tile_key(j - 1);
           if (rows_valid < BN) clear_v_tail_pair(st, rows_valid > 0 ? (int)rows_valid : 0);
           tc::fence_after_sync();
 #pragma unroll
@@ -392,7 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
     bool ok = true;
     int pv_seen = 0;  // P.V products whose completion this thread has consumed
     for (int j = 0; j < n_tiles; ++j) {
-      const int64_t kb = (kt0 + j) * BN;
+      const int64_t kb = tile_key(j);
       if (!wait_all(&ctl->s_full[j & 1], (j >> 1) & 1, abort_flag, deadline, a.status, 45, j)) {
         ok = false;
         break;
@@ -405,16 +416,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
       tc::tmem_wait_ld();
       // Logits arrive in log2 units (queries carry scale * log2 e). Keys this
       // row cannot see become -inf in place.
-      if (!(kb >= lo && kb + BN - 1 <= hi)) {
+      if (!((kb >= lo || (SK && kb + BN <= a.sinks)) && kb + BN - 1 <= hi)) {
         const int64_t dlo = lo - kb, dhi = hi - kb;
         const int c_lo = (int)(dlo < -1 ? -1 : dlo);
         const int c_hi = (int)(dhi > BN ? BN : dhi);
+        const int c_sink = SK ? (int)(a.sinks - kb > BN ? BN : a.sinks - kb) : 0;  // columns below it are sinks
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const int col = c * 32 + e;
-            if (col < c_lo || col > c_hi) r[c][e] = __float_as_uint(-INFINITY);
+            if ((col < c_lo && !(SK && col < c_sink)) || col > c_hi) r[c][e] = __float_as_uint(-INFINITY);
           }
       }
       // One speculative pass against the running max; a row redoes the tile
@@ -565,10 +577,11 @@ template <int D>
 cudaError_t launch_pair(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
                         const PairArgs& t, int B, cudaStream_t st) {
   using Cfg = PairCfg<D>;
-  cudaError_t e = cudaFuncSetAttribute(k_prefill_pair<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+  auto kern = t.sinks > 0 ? k_prefill_pair<D, true> : k_prefill_pair<D, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
   if (e != cudaSuccess) return e;
   dim3 grid(2 * t.n_pairs, (t.head_pair ? t.Hq / 2 : t.Hq) * Cfg::NV, B);
-  k_prefill_pair<D><<<grid, 192, Cfg::SMEM, st>>>(mq, mk, mv, mo, t);
+  kern<<<grid, 192, Cfg::SMEM, st>>>(mq, mk, mv, mo, t);
   return cudaGetLastError();
 }
 
@@ -583,6 +596,7 @@ cudaError_t launch_prefill_attn_pair(const PrefillAttnArgs& a, int B, int D, int
   PairArgs t;
   t.S = a.S;
   t.window = a.window;
+  t.sinks = a.sinks;
   t.Hq = a.Hq;
   t.Hkv = a.Hkv;
   t.key_cap = a.key_cap;

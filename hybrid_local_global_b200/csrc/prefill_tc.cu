@@ -87,6 +87,7 @@ struct TcCfg {
 
 struct TcArgs {
   int S, window, Hq, Hkv;
+  int sinks;  // SK instances: positions below it stay visible to every query
   int64_t key_cap;
   const int32_t* seq_lens_before;
   float scale_log2;
@@ -158,7 +159,9 @@ __device__ __forceinline__ float max_row(const uint32_t (&r)[4][32]) {
 // the G q heads of g for each of the `tokens` new tokens (rows past G *
 // tokens see no key), and it writes fp32 partials O / l and log2-sum-exp for
 // the combine instead of bf16 rows.
-template <int D, bool VF>
+// SK: a window plus sinks (cache views): the key tiles of the sinks, then the
+// tiles from the window's first one on.
+template <int D, bool VF, bool SK>
 __global__ void __launch_bounds__(192, 1)
     k_prefill_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -184,6 +187,7 @@ __global__ void __launch_bounds__(192, 1)
 
   int64_t pos0, n_keys, kt0;
   int n_tiles;
+  int n_st = 0;  // SK: tiles of the sinks, before tile kt0
   if (VF) {
     // token t sits at position seq_lens[b] - tokens + t; this CTA reads keys
     // [split * chunk, min(+chunk, seq_lens[b]))
@@ -207,7 +211,14 @@ __global__ void __launch_bounds__(192, 1)
     visible_range(pos0 + min(q0 + BM - 1, a.S - 1), a.window, n_keys, &lo_last, &hi_last);
     kt0 = lo_first / BN;
     n_tiles = (int)(hi_last / BN - kt0 + 1);
+    if (SK) {
+      const int64_t sink_tiles = ((int64_t)a.sinks + BN - 1) / BN;
+      n_st = (int)(sink_tiles < kt0 ? sink_tiles : kt0);
+      n_tiles += n_st;
+    }
   }
+  // first key of the j-th key tile
+  const auto tile_key = [&](int j) -> int64_t { return (SK && j < n_st ? j : kt0 + j - n_st) * BN; };
 
   if (threadIdx.x == 0) {
     mbar_init(&ctl->q_full, 1);
@@ -261,7 +272,7 @@ __global__ void __launch_bounds__(192, 1)
       for (int j = 0; j <= n_tiles && ok; ++j) {
         for (int kind = 0; kind < 2 && ok; ++kind) {  // 0: K_j, 1: V_{j-1}
           if ((kind == 0 && j == n_tiles) || (kind == 1 && j == 0)) continue;
-          int key0 = (int)((kt0 + j - kind) * BN - koff);  // view row
+          int key0 = (int)(tile_key(j - kind) - koff);  // view row
           int kb = b;                                           // view batch
           if (a.page_table) {
             // tiles never straddle a page (page_size is a multiple of 128); a
@@ -274,8 +285,8 @@ __global__ void __launch_bounds__(192, 1)
             }
             key0 -= pi * a.page_size;
           }
-          const int n_st = kind == 0 ? Cfg::K_STAGES : 2;
-          for (int half = 0; half < n_st; ++half, ++item) {
+          const int n_stg = kind == 0 ? Cfg::K_STAGES : 2;
+          for (int half = 0; half < n_stg; ++half, ++item) {
             const int s = item % NSTAGE;
             if (item >= NSTAGE &&
                 !mbar_wait_bounded_at(&ctl->empty[s], ((item / NSTAGE) - 1) & 1, abort_flag, deadline,
@@ -347,7 +358,7 @@ __global__ void __launch_bounds__(192, 1)
           ok = false;
           break;
         }
-        const int64_t tile_key0 = (kt0 + j - 1) * BN;
+        const int64_t tile_key0 = tile_key(j - 1);
         const uint32_t p_tm = tmem + COL_S + (uint32_t)((j - 1) & 1) * 128;
         for (int half = 0; half < 2; ++half, ++item) {
           const int s = item % NSTAGE;
@@ -410,7 +421,7 @@ __global__ void __launch_bounds__(192, 1)
     bool ok = true;
     int pv_seen = 0;  // P.V products whose completion this thread has consumed
     for (int j = 0; j < n_tiles; ++j) {
-      const int64_t kb = (kt0 + j) * BN;
+      const int64_t kb = tile_key(j);
       if (!wait_all(&ctl->s_full[j & 1], (j >> 1) & 1, abort_flag, deadline, a.status, 15, j)) {
         ok = false;
         break;
@@ -424,16 +435,17 @@ __global__ void __launch_bounds__(192, 1)
       // Logits arrive in log2 units (queries carry scale * log2 e). Keys this
       // row cannot see become -inf in place (only tiles that straddle the
       // visible range need it).
-      if (!(kb >= lo && kb + BN - 1 <= hi)) {
+      if (!((kb >= lo || (SK && kb + BN <= a.sinks)) && kb + BN - 1 <= hi)) {
         const int64_t dlo = lo - kb, dhi = hi - kb;
         const int c_lo = (int)(dlo < -1 ? -1 : dlo);
         const int c_hi = (int)(dhi > BN ? BN : dhi);
+        const int c_sink = SK ? (int)(a.sinks - kb > BN ? BN : a.sinks - kb) : 0;  // columns below it are sinks
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const int col = c * 32 + e;
-            if (col < c_lo || col > c_hi) r[c][e] = __float_as_uint(-INFINITY);
+            if ((col < c_lo && !(SK && col < c_sink)) || col > c_hi) r[c][e] = __float_as_uint(-INFINITY);
           }
       }
       // The running max m_used only moves when a tile's max exceeds it by more
@@ -597,6 +609,7 @@ cudaError_t launch_prefill_attn_tc(const PrefillAttnArgs& a, int B, int D, int k
   TcArgs t;
   t.S = a.S;
   t.window = a.window;
+  t.sinks = a.sinks;
   t.Hq = a.Hq;
   t.Hkv = a.Hkv;
   t.key_cap = a.key_cap;
@@ -615,18 +628,20 @@ cudaError_t launch_prefill_attn_tc(const PrefillAttnArgs& a, int B, int D, int k
   t.n_qtiles = (a.S + BM - 1) / BM;
   if (D == 256) {
     using Cfg = TcCfg<256>;
+    auto kern = a.sinks > 0 ? k_prefill_tc<256, false, true> : k_prefill_tc<256, false, false>;
     cudaError_t e =
-        cudaFuncSetAttribute(k_prefill_tc<256, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
     if (e != cudaSuccess) return e;
     dim3 grid(a.Hq * Cfg::NV, B, t.n_qtiles);
-    k_prefill_tc<256, false><<<grid, 192, Cfg::SMEM, st>>>(mq, mk, mv, mo, t);
+    kern<<<grid, 192, Cfg::SMEM, st>>>(mq, mk, mv, mo, t);
   } else {
     using Cfg = TcCfg<512>;
+    auto kern = a.sinks > 0 ? k_prefill_tc<512, false, true> : k_prefill_tc<512, false, false>;
     cudaError_t e =
-        cudaFuncSetAttribute(k_prefill_tc<512, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
     if (e != cudaSuccess) return e;
     dim3 grid(a.Hq * Cfg::NV, B, t.n_qtiles);
-    k_prefill_tc<512, false><<<grid, 192, Cfg::SMEM, st>>>(mq, mk, mv, mo, t);
+    kern<<<grid, 192, Cfg::SMEM, st>>>(mq, mk, mv, mo, t);
   }
   return cudaGetLastError();
 }
@@ -636,10 +651,10 @@ template <int D>
 cudaError_t launch_verify_as(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const TcArgs& t,
                              int B, cudaStream_t st) {
   using Cfg = TcCfg<D>;
-  cudaError_t e = cudaFuncSetAttribute(k_prefill_tc<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(k_prefill_tc<D, true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
   if (e != cudaSuccess) return e;
   dim3 grid(t.Hkv * Cfg::NV, B, t.n_splits);
-  k_prefill_tc<D, true><<<grid, 192, Cfg::SMEM, st>>>(mq, mk, mv, mq, t);
+  k_prefill_tc<D, true, false><<<grid, 192, Cfg::SMEM, st>>>(mq, mk, mv, mq, t);
   return cudaGetLastError();
 }
 }  // namespace

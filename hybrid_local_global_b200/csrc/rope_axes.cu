@@ -1,0 +1,177 @@
+// rope_axes.cu -- rotary positions with several axes (time, height, width of
+// image and video tokens), and the inverse rotation.
+//
+// Pair i = (x_2i, x_2i+1) of every head vector of token t turns by the angle
+//   pos[axis(i)][t] * freq(i),
+// freq(i) = theta^(-2i/D) as the attention calls use, or theta^(-r/n) for the
+// r-th of an axis's n pairs (a vision encoder's two-axis form: half of a patch
+// embedding turns by x, the other by y; "Gemma 4: End-to-End Architecture
+// Walkthrough", 2). A rotation is orthogonal: its gradient and its inverse are
+// the rotation by the opposite angle.
+//
+// Precision: as in rope_kv.cu the angle is formed and reduced in fp64, in
+// half-turns (an fp32 product has an ulp of 1/64 rad near position 2.6e5); the
+// sine and cosine of the reduced angle and the rotation are fp32, and the
+// result is rounded to bf16 once.
+//
+// Bound by HBM: every vector is read and written once. The angles of a token
+// are the same for all of its heads, so a CTA forms them once per token in
+// shared memory.
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace hlg {
+
+namespace {
+
+constexpr int MAX_PAIRS = 256;
+constexpr int MAX_AXES = 4;
+constexpr int AX_T = 256;
+
+struct AxesArgs {
+  double freq[MAX_PAIRS];  // half-turns per position; negated for the inverse
+  unsigned char axis[MAX_PAIRS];
+  const bf16* q;
+  const bf16* k;
+  bf16* q_out;
+  bf16* k_out;
+  long long q_stride, k_stride, q_out_stride, k_out_stride;  // elements between tokens
+  const int32_t* pos;  // [n_axes][tokens]
+  int tokens, Hq, Hkv, D, n_rot;
+};
+
+// grid.x strides over tokens. Thread (c, r): 8 elements c of head vectors
+// r, r + R, ... of the token.
+__global__ void __launch_bounds__(AX_T) k_rope_axes(const __grid_constant__ AxesArgs a) {
+  __shared__ float2 trig[MAX_PAIRS];
+  const int C = a.D / 8, R = AX_T / C;
+  const int c = threadIdx.x % C, r = threadIdx.x / C;
+  const int H = a.Hq + a.Hkv;
+  for (int t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+    __syncthreads();  // the previous token's angles have been read
+    for (int i = threadIdx.x; i < a.n_rot; i += AX_T) {
+      const double x = (double)a.pos[(int64_t)a.axis[i] * a.tokens + t] * a.freq[i];
+      float s, co;
+      sincospif((float)(x - 2.0 * rint(0.5 * x)), &s, &co);
+      trig[i] = make_float2(co, s);
+    }
+    __syncthreads();
+    if (r >= R) continue;
+    float2 cs[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) cs[j] = c * 4 + j < a.n_rot ? trig[c * 4 + j] : make_float2(1.f, 0.f);
+    for (int h = r; h < H; h += R) {
+      const bool is_q = h < a.Hq;
+      const bf16* src = is_q ? a.q + t * a.q_stride + h * a.D : a.k + t * a.k_stride + (h - a.Hq) * a.D;
+      bf16* dst = is_q ? a.q_out + t * a.q_out_stride + h * a.D : a.k_out + t * a.k_out_stride + (h - a.Hq) * a.D;
+      uint4 v = *reinterpret_cast<const uint4*>(src + c * 8);
+      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c * 4 + j < a.n_rot) {
+          const float2 x = unpack_bf16x2(w[j]);
+          w[j] = pack_bf16x2(x.x * cs[j].x - x.y * cs[j].y, x.x * cs[j].y + x.y * cs[j].x);
+        }
+      *reinterpret_cast<uint4*>(dst + c * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+int err(int code, const char* msg) { return record_error(code, msg); }
+
+// Strided vectors [tokens][heads][D]: 16-byte loads need every token to start
+// on 16 bytes; a token's heads are dense.
+int check_side(const void* p, long long stride, const void* out, long long out_stride, int tokens, int heads, int D) {
+  if (!p || !out) return err(GEMMA_ERR_INVALID_ARG, "null tensor pointer");
+  if ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(out)) & 15u || (stride | out_stride) % 8)
+    return err(GEMMA_ERR_INVALID_ARG, "tensors must be 16-byte aligned with token strides of a multiple of 8 elements");
+  const long long row = (long long)heads * D;
+  if (tokens > 1 && (stride < row || out_stride < row))
+    return err(GEMMA_ERR_INVALID_ARG, "a token stride is smaller than heads * head_dim");
+  // in place, or apart
+  const char* a = static_cast<const char*>(p);
+  const char* b = static_cast<const char*>(out);
+  const long long na = ((tokens - 1) * stride + row) * 2, nb = ((tokens - 1) * out_stride + row) * 2;
+  if (a == b ? (tokens > 1 && stride != out_stride) : (a < b + nb && b < a + na))
+    return err(GEMMA_ERR_INVALID_ARG, "an output must be its input (same stride) or must not overlap it");
+  return GEMMA_OK;
+}
+
+}  // namespace
+}  // namespace hlg
+
+using namespace hlg;
+
+extern "C" int gemma_rope_axes(const void* q, long long q_stride, const void* k, long long k_stride,
+                               const int32_t* positions, int n_axes, const int* axis_pairs, int tokens, int n_q_heads,
+                               int n_kv_heads, int head_dim, float rope_theta, void* q_out, long long q_out_stride,
+                               void* k_out, long long k_out_stride, unsigned flags, void* stream) {
+  if (flags & ~(GEMMA_ROPE_INTERLEAVED | GEMMA_ROPE_AXIS_LADDERS | GEMMA_ROPE_INVERSE))
+    return err(GEMMA_ERR_INVALID_ARG, "unknown flags");
+  if (tokens < 0 || n_q_heads <= 0 || n_kv_heads < 0)
+    return err(GEMMA_ERR_INVALID_ARG, "tokens, n_q_heads or n_kv_heads out of range");
+  if (head_dim <= 0 || head_dim % 8 || head_dim > 2 * MAX_PAIRS)
+    return err(GEMMA_ERR_UNSUPPORTED, "head_dim must be a multiple of 8, at most 512");
+  if ((long long)(n_q_heads + (long long)n_kv_heads) * head_dim > (1 << 30))
+    return err(GEMMA_ERR_UNSUPPORTED, "heads * head_dim exceeds 2^30");
+  if (n_axes < 1 || n_axes > MAX_AXES || !axis_pairs) return err(GEMMA_ERR_INVALID_ARG, "n_axes must be 1 to 4");
+  if (!(rope_theta > 0.f) || !std::isfinite(rope_theta))
+    return err(GEMMA_ERR_INVALID_ARG, "rope_theta must be positive and finite");
+  long long n_rot = 0;
+  for (int x = 0; x < n_axes; ++x) {
+    if (axis_pairs[x] < 0) return err(GEMMA_ERR_INVALID_ARG, "axis_pairs must not be negative");
+    n_rot += axis_pairs[x];
+  }
+  if (n_rot > head_dim / 2) return err(GEMMA_ERR_INVALID_ARG, "axis_pairs sum to more than head_dim / 2");
+  if (tokens == 0) return record_ok();
+  if (!positions || reinterpret_cast<uintptr_t>(positions) & 3u)
+    return err(GEMMA_ERR_INVALID_ARG, "positions: null or misaligned pointer");
+  int rc = check_side(q, q_stride, q_out, q_out_stride, tokens, n_q_heads, head_dim);
+  if (!rc && n_kv_heads) rc = check_side(k, k_stride, k_out, k_out_stride, tokens, n_kv_heads, head_dim);
+  if (rc) return rc;
+
+  AxesArgs a;
+  int i = 0;
+  const auto put = [&](int x, int rank) {
+    const double expo = (flags & GEMMA_ROPE_AXIS_LADDERS) ? (double)rank / axis_pairs[x] : 2.0 * i / head_dim;
+    const double f = std::pow((double)rope_theta, -expo) * 0.31830988618379067153776752674503;  // / pi
+    a.freq[i] = (flags & GEMMA_ROPE_INVERSE) ? -f : f;
+    a.axis[i] = (unsigned char)x;
+    ++i;
+  };
+  if (flags & GEMMA_ROPE_INTERLEAVED) {
+    for (int rank = 0; i < n_rot; ++rank)
+      for (int x = 0; x < n_axes; ++x)
+        if (rank < axis_pairs[x]) put(x, rank);
+  } else {
+    for (int x = 0; x < n_axes; ++x)
+      for (int rank = 0; rank < axis_pairs[x]; ++rank) put(x, rank);
+  }
+  a.n_rot = (int)n_rot;
+  a.q = static_cast<const bf16*>(q);
+  a.k = static_cast<const bf16*>(k);
+  a.q_out = static_cast<bf16*>(q_out);
+  a.k_out = static_cast<bf16*>(k_out);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.q_out_stride = q_out_stride;
+  a.k_out_stride = k_out_stride;
+  a.pos = positions;
+  a.tokens = tokens;
+  a.Hq = n_q_heads;
+  a.Hkv = n_kv_heads;
+  a.D = head_dim;
+  const int grid = std::min(tokens, multiprocessors() * 8);
+  k_rope_axes<<<grid, AX_T, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    char m[256];
+    snprintf(m, sizeof m, "multi-axis rotation launch: %s", cudaGetErrorString(e));
+    return err(GEMMA_ERR_CUDA, m);
+  }
+  return record_ok();
+}

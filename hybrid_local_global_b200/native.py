@@ -9,6 +9,7 @@ the import fails.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -401,3 +402,304 @@ def gemma_attn_decode_noalloc(q, k_new, v_new, k_cache, v_cache, *, seq_lens, ma
     return _check(_decode_noalloc(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), cap,
                                   _ptr(seq_lens), max_seq_len, B, window, Hq, Hkv, D, rope_frac,
                                   rope_theta, scale, _ptr(out), flags, _stream(stream)))
+
+
+# ------------------------------------------------- window plus sinks, pages, axes
+GEMMA_ROPE_INTERLEAVED = 1  # pairs go to the axes in turn
+GEMMA_ROPE_AXIS_LADDERS = 2  # every axis has the whole range of frequencies
+GEMMA_ROPE_INVERSE = 4  # the opposite rotation: gradient and inverse
+
+_LL = ctypes.c_longlong
+
+
+class gemma_page_book(ctypes.Structure):
+    _fields_ = [("page_table", _P), ("ref_count", _P), ("n_seqs", _I), ("pages_per_seq", _I), ("n_pages", _I),
+                ("page_size", _I)]
+
+
+class gemma_page_pool(ctypes.Structure):
+    _fields_ = [("pool", _P), ("n_kv_heads", _I), ("head_dim", _I), ("flags", ctypes.c_uint)]
+
+
+_BOOK = ctypes.POINTER(gemma_page_book)
+_POOLS = ctypes.POINTER(gemma_page_pool)
+_prefill_sinks = _sig("gemma_attn_prefill_sinks", _I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _I, _I, _I, _I, _I, _I,
+                                                       _I, _F, _F, _F, _P, _P, _P, _SZ, ctypes.c_uint, _P])
+_decode_sinks_ws = _sig("gemma_attn_decode_sinks_workspace_size", _SZ, [_I, _I, _I, _I, _I, _I, _I])
+_decode_sinks = _sig("gemma_attn_decode_sinks", _I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _I, _I, _I, _I, _I, _I,
+                                                     _I, _F, _F, _F, _P, _P, _SZ, ctypes.c_uint, _P])
+_pages_ws = _sig("gemma_kv_pages_workspace_size", _SZ, [_I, _I, _I])
+_pages_fork = _sig("gemma_kv_pages_fork", _I, [_BOOK, _P, _P])
+_pages_reserve = _sig("gemma_kv_pages_reserve", _I, [_BOOK, _POOLS, _I, _P, _P, _P, _P, _SZ, _P])
+_pages_trim = _sig("gemma_kv_pages_trim", _I, [_BOOK, _P, _I, _I, _P])
+_pages_compact = _sig("gemma_kv_pages_compact", _I, [_BOOK, _POOLS, _I, _P, _P, _P, _SZ, _P])
+_pages_copy = _sig("gemma_kv_pages_copy", _I, [_POOLS, _I, _I, _I, _P, _P, _I, _P])
+_rope_axes = _sig("gemma_rope_axes", _I, [_P, _LL, _P, _LL, _P, _I, ctypes.POINTER(_I), _I, _I, _I, _I, _F, _P, _LL,
+                                          _P, _LL, ctypes.c_uint, _P])
+EXPORTED += ["gemma_attn_prefill_sinks", "gemma_attn_decode_sinks_workspace_size", "gemma_attn_decode_sinks",
+             "gemma_kv_pages_workspace_size", "gemma_kv_pages_fork", "gemma_kv_pages_reserve", "gemma_kv_pages_trim",
+             "gemma_kv_pages_compact", "gemma_kv_pages_copy", "gemma_rope_axes"]
+
+
+def _on(device, stream, what):
+    """The device guard of a call whose tensors are on `device`, and its
+    stream: that device's current one by default."""
+    if device.type != "cuda":
+        raise TypeError("%s: tensors must be on a CUDA device, not %s" % (what, device))
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError("%s: stream of %s, tensors on %s" % (what, stream.device, device))
+    return torch.cuda.device(device), ctypes.c_void_p(stream.cuda_stream)
+
+
+def _need(t, name, dtype, shape, device):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise TypeError("%s must be a contiguous %s tensor on %s" % (name, dtype, device))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape), tuple(shape)))
+
+
+def _sinks_args(q, k_new, v_new, k_pool, v_pool, page_table, out, lens, lens_name, flags):
+    """Shapes and devices of a window-plus-sinks call: (B, new token dims, Hq,
+    Hkv, D, page_size, pages_per_seq, n_pages, flags)."""
+    if isinstance(k_pool, Int8KVCache) or isinstance(v_pool, Int8KVCache):
+        flags |= _kv_kind(k_pool, v_pool)
+    for t, n in ((q, "q"), (k_new, "k_new"), (v_new, "v_new"), (k_pool, "k_pool"), (v_pool, "v_pool"), (out, "out")):
+        _bf16(t, n)
+    dev = q.device
+    B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
+    n_pages, Hkv, ps, pps = _paged_args(k_pool, page_table)
+    _need(page_table, "page_table", torch.int32, (B, pps), dev)
+    if k_pool.shape[-1] != D or (v_pool is not None and tuple(v_pool.shape) != tuple(k_pool.shape)):
+        raise ValueError("k_pool and v_pool must be [n_pages, Hkv, page_size, D] with the D of q")
+    for t, n in ((k_pool, "k_pool"), (v_pool, "v_pool")):
+        if t is not None and t.device != dev:
+            raise TypeError("%s is on %s, q on %s" % (n, t.device, dev))
+    for t, n in ((k_new, "k_new"), (v_new, "v_new")):
+        if t is not None:
+            _need(t, n, torch.bfloat16, (*q.shape[:-2], Hkv, D), dev)
+    _need(out, "out", torch.bfloat16, q.shape, dev)
+    if lens is not None:
+        _need(lens, lens_name, torch.int32, (B,), dev)
+    return B, Hq, Hkv, D, ps, pps, n_pages, flags
+
+
+def _workspace(workspace, size, device):
+    if workspace is None:
+        return torch.empty(max(size, 1), dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous tensor on %s" % device)
+    return workspace
+
+
+def gemma_attn_prefill_sinks(q, k_new, v_new, k_pool, v_pool, page_table, *, window, sinks, rope_frac, rope_theta,
+                             scale, out, seq_lens_before=None, lse=None, workspace=None, flags=0, stream=None):
+    """A chunk on a paged layer that sees the last `window` positions and the
+    first `sinks`: tensors as gemma_attn_prefill_paged (bf16 pools)."""
+    B, Hq, Hkv, D, ps, pps, n_pages, flags = _sinks_args(q, k_new, v_new, k_pool, v_pool, page_table, out,
+                                                         seq_lens_before, "seq_lens_before", flags)
+    S = q.shape[1]
+    if q.dim() != 4:
+        raise ValueError("q must be [B, S, Hq, D]")
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (B, Hq, S), q.device)
+    workspace = _workspace(workspace, gemma_attn_prefill_workspace_size(B, S, Hq, Hkv, D, 0), q.device)
+    guard, st = _on(q.device, stream, "gemma_attn_prefill_sinks")
+    with guard:
+        return _check(_prefill_sinks(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool), _ptr(v_pool), _ptr(page_table),
+                                     ps, pps, n_pages, _ptr(seq_lens_before), B, S, window, sinks, Hq, Hkv, D,
+                                     rope_frac, rope_theta, scale, _ptr(out), _ptr(lse), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(), flags, st))
+
+
+def gemma_attn_decode_sinks_workspace_size(batch, n_q_heads, n_kv_heads, head_dim, window, sinks, max_seq_len) -> int:
+    return int(_decode_sinks_ws(batch, n_q_heads, n_kv_heads, head_dim, window, sinks, max_seq_len))
+
+
+def gemma_attn_decode_sinks(q, k_new, v_new, k_pool, v_pool, page_table, *, seq_lens, max_seq_len, window, sinks,
+                            rope_frac, rope_theta, scale, out, workspace=None, flags=0, stream=None):
+    """One new token per sequence on a paged layer that sees the last `window`
+    positions and the first `sinks`: tensors as gemma_attn_decode_paged (bf16
+    pools); seq_lens 0 marks an idle slot."""
+    if seq_lens is None:
+        raise TypeError("seq_lens is required")
+    B, Hq, Hkv, D, ps, pps, n_pages, flags = _sinks_args(q, k_new, v_new, k_pool, v_pool, page_table, out, seq_lens,
+                                                         "seq_lens", flags)
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, D]")
+    workspace = _workspace(workspace, gemma_attn_decode_sinks_workspace_size(B, Hq, Hkv, D, window, sinks, max_seq_len),
+                           q.device)
+    guard, st = _on(q.device, stream, "gemma_attn_decode_sinks")
+    with guard:
+        return _check(_decode_sinks(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool), _ptr(v_pool), _ptr(page_table),
+                                    ps, pps, n_pages, _ptr(seq_lens), max_seq_len, B, window, sinks, Hq, Hkv, D,
+                                    rope_frac, rope_theta, scale, _ptr(out), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), flags, st))
+
+
+class PageBook:
+    """Page table and reference counts of a paged cache, on the device:
+    ``page_table`` int32 [n_seqs, pages_per_seq] (-1: no page) and
+    ``ref_count`` int32 [n_pages], both views of ``state`` (one int32 tensor, so
+    that a book is saved and restored with one copy). Starts empty."""
+
+    def __init__(self, n_seqs, pages_per_seq, n_pages, page_size, device):
+        n = n_seqs * pages_per_seq
+        self.state = torch.zeros(n + n_pages, dtype=torch.int32, device=device)
+        self.page_table = self.state[:n].view(n_seqs, pages_per_seq)
+        self.ref_count = self.state[n:]
+        self.page_table.fill_(-1)
+        self.page_size = page_size
+        self.device = self.state.device
+        self.desc = gemma_page_book(self.page_table.data_ptr(), self.ref_count.data_ptr(), n_seqs, pages_per_seq,
+                                    n_pages, page_size)
+
+    @property
+    def n_seqs(self):
+        return self.page_table.shape[0]
+
+    @property
+    def pages_per_seq(self):
+        return self.page_table.shape[1]
+
+    @property
+    def n_pages(self):
+        return self.ref_count.shape[0]
+
+
+def _book(book):
+    return ctypes.byref(book.desc)
+
+
+def _pool_list(pools, n_pages, page_size, device):
+    """gemma_page_pool array of bf16 tensors [n_pages, Hkv, page_size, D] and
+    Int8KVCache(n_pages, Hkv, page_size, D) buffers."""
+    arr = (gemma_page_pool * max(len(pools), 1))()
+    for i, p in enumerate(pools):
+        q8 = isinstance(p, Int8KVCache)
+        _bf16(p, "pool")
+        if len(p.shape) != 4 or p.shape[0] != n_pages or p.shape[2] != page_size:
+            raise ValueError("pool %d must be [n_pages %d, Hkv, page_size %d, D]" % (i, n_pages, page_size))
+        if p.device != device:
+            raise TypeError("pool %d is on %s, not %s" % (i, p.device, device))
+        arr[i].pool, arr[i].n_kv_heads, arr[i].head_dim = p.data_ptr(), p.shape[1], p.shape[3]
+        arr[i].flags = GEMMA_F_KV_INT8 if q8 else 0
+    return arr
+
+
+def gemma_kv_pages_workspace_size(n_seqs, pages_per_seq, n_pages) -> int:
+    return int(_pages_ws(n_seqs, pages_per_seq, n_pages))
+
+
+def gemma_kv_pages_fork(book, parents, *, stream=None):
+    """Row b of the book's table becomes row parents[b] (int32 [n_seqs]; b: unchanged, -1: empty)."""
+    _need(parents, "parents", torch.int32, (book.n_seqs,), book.device)
+    guard, st = _on(book.device, stream, "gemma_kv_pages_fork")
+    with guard:
+        return _check(_pages_fork(_book(book), _ptr(parents), st))
+
+
+def gemma_kv_pages_reserve(book, pools, *, seq_lens, new_tokens, lacking, workspace=None, stream=None):
+    """Grants pages (copying shared ones that will be written) for positions
+    seq_lens[b] .. + new_tokens[b] of every row; lacking int32 [1] receives
+    how many pages are missing (then nothing was changed)."""
+    dev = book.device
+    _need(seq_lens, "seq_lens", torch.int32, (book.n_seqs,), dev)
+    _need(new_tokens, "new_tokens", torch.int32, (book.n_seqs,), dev)
+    _need(lacking, "lacking", torch.int32, (1,), dev)
+    arr = _pool_list(pools, book.n_pages, book.page_size, dev)
+    workspace = _workspace(workspace, gemma_kv_pages_workspace_size(book.n_seqs, book.pages_per_seq, book.n_pages), dev)
+    guard, st = _on(dev, stream, "gemma_kv_pages_reserve")
+    with guard:
+        return _check(_pages_reserve(_book(book), arr, len(pools), _ptr(seq_lens), _ptr(new_tokens), _ptr(lacking),
+                                     _ptr(workspace), workspace.numel() * workspace.element_size(), st))
+
+
+def gemma_kv_pages_trim(book, *, seq_lens, window=0, sinks=0, stream=None):
+    """Drops the pages that hold nothing a token after seq_lens[b] sees
+    (int32 [n_seqs]; 0 ends the sequence, below 0 leaves its row alone)."""
+    _need(seq_lens, "seq_lens", torch.int32, (book.n_seqs,), book.device)
+    guard, st = _on(book.device, stream, "gemma_kv_pages_trim")
+    with guard:
+        return _check(_pages_trim(_book(book), _ptr(seq_lens), window, sinks, st))
+
+
+def gemma_kv_pages_compact(book, pools, *, n_live, page_map=None, workspace=None, stream=None):
+    """Moves the live pages to numbers 0 .. n_live - 1 (n_live int32 [1],
+    written); page_map int32 [n_pages]: the new number of every live page."""
+    dev = book.device
+    _need(n_live, "n_live", torch.int32, (1,), dev)
+    if page_map is not None:
+        _need(page_map, "page_map", torch.int32, (book.n_pages,), dev)
+    arr = _pool_list(pools, book.n_pages, book.page_size, dev)
+    workspace = _workspace(workspace, gemma_kv_pages_workspace_size(book.n_seqs, book.pages_per_seq, book.n_pages), dev)
+    guard, st = _on(dev, stream, "gemma_kv_pages_compact")
+    with guard:
+        return _check(_pages_compact(_book(book), arr, len(pools), _ptr(n_live), _ptr(page_map), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(), st))
+
+
+def gemma_kv_pages_copy(pools, *, src, dst, stream=None):
+    """Copies pages src[i] -> dst[i] (int32 [n]) in every pool of the list."""
+    if not pools:
+        raise ValueError("no pools")
+    dev = pools[0].device
+    n_pages, _, page_size, _ = pools[0].shape
+    if src.dim() != 1:
+        raise ValueError("src must be one-dimensional")
+    _need(src, "src", torch.int32, src.shape, dev)
+    _need(dst, "dst", torch.int32, src.shape, dev)
+    arr = _pool_list(pools, n_pages, page_size, dev)
+    guard, st = _on(dev, stream, "gemma_kv_pages_copy")
+    with guard:
+        return _check(_pages_copy(arr, len(pools), n_pages, page_size, _ptr(src), _ptr(dst), src.numel(), st))
+
+
+def _token_rows(t, name, heads_dim):
+    """(token stride, heads) of [..., heads, D] whose heads are dense and whose
+    leading dimensions step evenly."""
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() < 3:
+        raise TypeError("%s must be a bf16 CUDA tensor [..., heads, head_dim]" % name)
+    H, D = t.shape[-2:]
+    if D != heads_dim:
+        raise ValueError("%s has head_dim %d, not %d" % (name, D, heads_dim))
+    lead = [(n, s) for n, s in zip(t.shape[:-2], t.stride()[:-2]) if n != 1]
+    ok = t.numel() == 0 or ((D == 1 or t.stride(-1) == 1) and (H == 1 or t.stride(-2) == D))
+    for (_, s0), (n1, s1) in zip(lead, lead[1:]):
+        ok = ok and s0 == n1 * s1
+    if not ok and t.numel():
+        raise ValueError("%s: heads must be dense and tokens evenly spaced" % name)
+    return (lead[-1][1] if lead else H * D), H
+
+
+def gemma_rope_axes(q, k, positions, *, axis_pairs, rope_theta, q_out, k_out=None, flags=0, stream=None):
+    """Rotary positions with several axes: q [..., Hq, D] and k [..., Hkv, D]
+    (or None) turned by positions int32 [n_axes, ...] into q_out and k_out
+    (which may be q and k). Tokens may be strided, e.g. slices of a fused
+    projection; see GEMMA_ROPE_* for flags."""
+    D = q.shape[-1]
+    qs, Hq = _token_rows(q, "q", D)
+    qos, _ = _token_rows(q_out, "q_out", D)
+    tokens = math.prod(q.shape[:-2])
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have the shape of q")
+    ks = kos = Hkv = 0
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    if k is not None:
+        ks, Hkv = _token_rows(k, "k", D)
+        kos, _ = _token_rows(k_out, "k_out", D)
+        if k.shape[:-2] != q.shape[:-2] or k_out.shape != k.shape:
+            raise ValueError("k and k_out must have the tokens of q")
+    dev = q.device
+    for t, n in ((q_out, "q_out"), (k, "k"), (k_out, "k_out")):
+        if t is not None and t.device != dev:
+            raise TypeError("%s is on %s, q on %s" % (n, t.device, dev))
+    n_axes = len(axis_pairs)
+    _need(positions, "positions", torch.int32, (n_axes, *q.shape[:-2]), dev)
+    pairs = (_I * max(n_axes, 1))(*axis_pairs)
+    guard, st = _on(dev, stream, "gemma_rope_axes")
+    with guard:
+        return _check(_rope_axes(_ptr(q), qs, _ptr(k), ks, _ptr(positions), n_axes, pairs, tokens, Hq, Hkv, D,
+                                 rope_theta, _ptr(q_out), qos, _ptr(k_out), kos, flags, st))

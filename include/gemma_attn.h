@@ -316,6 +316,167 @@ int gemma_attn_decode_multi_paged(const void* q, const void* k_new, const void* 
                                   size_t workspace_bytes, unsigned flags, void* stream);
 
 /* ---------------------------------------------------------------------- */
+/* Window plus sinks on a paged cache: a layer whose queries see the last  */
+/* `window` positions ("Gemma 4: End-to-End Architecture Walkthrough", 3a) */
+/* and, for good, the sequence's first `sinks` ones. Key j is visible to   */
+/* the query at position p iff j <= p and (j > p - window or j < sinks).    */
+/* Positions stay absolute; pages that hold no visible position may be      */
+/* given back (gemma_kv_pages_trim), so a layer's cache stays bounded        */
+/* however long the sequence grows.                                          */
+/* Arguments and behaviour as gemma_attn_prefill_paged /                    */
+/* gemma_attn_decode_paged, except:                                         */
+/* window >= 1 (any number), sinks >= 0.                                    */
+/* page_table: entries of pages that hold no position visible to the call  */
+/*        and none that it writes are not used, and may hold anything.      */
+/* seq_lens (decode): 0 marks an idle slot of the batch: its out is zeros, */
+/*        nothing is written for it and it is no error. A length below 0 or */
+/*        above max_seq_len gives zeros and GEMMA_ERR_DEVICE_RANGE.          */
+/* Values at positions that no query of the call sees are not used, what-   */
+/* ever they hold, with one exception: in prefill a position that shares a  */
+/* 128-position block with a visible one must hold finite values.            */
+/* flags: GEMMA_F_SHARED, GEMMA_F_KEQV. bf16 pools only (GEMMA_F_KV_INT8:   */
+/*        GEMMA_ERR_UNSUPPORTED). No two sequences of a call may write the  */
+/*        same page (gemma_kv_pages_reserve sees to that).                   */
+/* Prefill workspace: gemma_attn_prefill_workspace_size(batch, s_new,       */
+/* n_q_heads, n_kv_heads, head_dim, 0). Decode is one launch and uses no    */
+/* workspace today: the size is 0 and workspace may then be NULL.            */
+/* ---------------------------------------------------------------------- */
+int gemma_attn_prefill_sinks(const void* q, const void* k_new, const void* v_new,
+                             void* k_pool, void* v_pool, const int32_t* page_table,
+                             int page_size, int pages_per_seq, int n_pages,
+                             const int32_t* seq_lens_before, int batch, int s_new, int window,
+                             int sinks, int n_q_heads, int n_kv_heads, int head_dim,
+                             float rope_frac, float rope_theta, float scale, void* out, float* lse,
+                             void* workspace, size_t workspace_bytes, unsigned flags,
+                             void* stream);
+size_t gemma_attn_decode_sinks_workspace_size(int batch, int n_q_heads, int n_kv_heads,
+                                              int head_dim, int window, int sinks,
+                                              int max_seq_len);
+int gemma_attn_decode_sinks(const void* q, const void* k_new, const void* v_new,
+                            void* k_pool, void* v_pool, const int32_t* page_table,
+                            int page_size, int pages_per_seq, int n_pages,
+                            const int32_t* seq_lens, int max_seq_len, int batch, int window,
+                            int sinks, int n_q_heads, int n_kv_heads, int head_dim,
+                            float rope_frac, float rope_theta, float scale, void* out,
+                            void* workspace, size_t workspace_bytes, unsigned flags,
+                            void* stream);
+
+/* ---------------------------------------------------------------------- */
+/* Page upkeep for paged caches, on the device and in stream order (every  */
+/* call can be captured into a graph). The caller owns all memory.          */
+/* ---------------------------------------------------------------------- */
+typedef struct gemma_page_book {
+    int32_t* page_table; /* device [n_seqs][pages_per_seq]; -1: no page */
+    int32_t* ref_count;  /* device [n_pages]: table entries that name the page; 0: free */
+    int n_seqs;          /* at most 4096 */
+    int pages_per_seq;   /* n_seqs * pages_per_seq at most 2^30 */
+    int n_pages;         /* at most 2^20 */
+    int page_size;       /* positions per page, a multiple of 128 */
+} gemma_page_book;       /* an empty book: every entry -1, every count 0 */
+
+/* One pool of pages that the book's page numbers index: a layer's K or V
+ * pool (under K = V the K pool alone; a shared layer's pool once). head_dim
+ * must be a multiple of 16. All page calls move the same pages of every pool
+ * listed; pools must not overlap, except that a pool may be listed twice. */
+typedef struct gemma_page_pool {
+    void* pool;     /* [n_pages][n_kv_heads][page_size][head_dim] bf16, or a GEMMA_F_KV_INT8 buffer */
+    int n_kv_heads;
+    int head_dim;
+    unsigned flags; /* 0 or GEMMA_F_KV_INT8 */
+} gemma_page_pool;
+
+/* Workspace of gemma_kv_pages_reserve and gemma_kv_pages_compact on such a
+ * book (scratch, 16-byte aligned). 0 on bad arguments. */
+size_t gemma_kv_pages_workspace_size(int n_seqs, int pages_per_seq, int n_pages);
+
+/* Fork: row b of the table becomes what row parents[b] was before the call
+ * (device int32 [n_seqs]); b itself keeps the row, -1 empties it. All rows at
+ * once, so a beam search's reordering is one call; a row that several rows
+ * name is shared between them. Page contents do not move: before new tokens
+ * are written, gemma_kv_pages_reserve gives each sharer its own last page.
+ * A parent outside [-1, n_seqs) leaves its row alone and reports
+ * GEMMA_ERR_DEVICE_RANGE. */
+int gemma_kv_pages_fork(const gemma_page_book* book, const int32_t* parents, void* stream);
+
+/* Reserve: makes positions [seq_lens[b], seq_lens[b] + new_tokens[b]) of every
+ * row b writable (device int32 [n_seqs] each; new_tokens 0: nothing for that
+ * row). Missing pages are granted, the lowest free page numbers in (row,
+ * entry) order. An entry whose page other entries name too is replaced by a
+ * fresh page (copy on write): the rows of it that the sequence holds (below
+ * seq_lens[b]) are copied in every pool, its other rows are left as they
+ * were. Of the sharers, the last one in (row, entry) order keeps the page when
+ * no entry outside the call names it.
+ * *lacking (device int32) becomes 0; when the free pages do not suffice it
+ * becomes the number that is missing, nothing at all is changed, and
+ * GEMMA_ERR_DEVICE_RANGE is reported. A row with a negative count or length,
+ * or with more positions than the table holds, is left out and reported. */
+int gemma_kv_pages_reserve(const gemma_page_book* book, const gemma_page_pool* pools, int n_pools,
+                           const int32_t* seq_lens, const int32_t* new_tokens, int32_t* lacking,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Trim: drops the entries of row b whose page holds none of the positions
+ * below seq_lens[b] (device int32 [n_seqs]) that a later token can see:
+ * window == 0: every position; else j > seq_lens[b] - window or j < sinks. So
+ * it frees what fell out of a window, shortens a sequence (rejected tokens),
+ * or with length 0 ends it. A negative length leaves its row alone; one above
+ * the table's capacity does too and reports GEMMA_ERR_DEVICE_RANGE. */
+int gemma_kv_pages_trim(const gemma_page_book* book, const int32_t* seq_lens, int window, int sinks,
+                        void* stream);
+
+/* Compact: moves live pages so that they are the pages 0 .. *n_live - 1
+ * (device int32), in the table, the counts and every pool: the k-th live page
+ * numbered *n_live or more goes into the k-th free one below. page_map
+ * (device int32 [n_pages], or NULL): the new number of every page that was
+ * live, -1 for the others. An entry that names no live page is left alone and
+ * reported (GEMMA_ERR_DEVICE_RANGE). */
+int gemma_kv_pages_compact(const gemma_page_book* book, const gemma_page_pool* pools, int n_pools,
+                           int32_t* n_live, int32_t* page_map, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Copy pages src[i] -> dst[i] (device int32 [n_copies]) in every pool; tables
+ * and counts are not involved. A pair is carried out iff both pages exist, no
+ * other pair names the same destination, and no other pair with a different
+ * source and destination writes its source; others are skipped and reported
+ * (GEMMA_ERR_DEVICE_RANGE). src[i] == dst[i] copies nothing. */
+int gemma_kv_pages_copy(const gemma_page_pool* pools, int n_pools, int n_pages, int page_size,
+                        const int32_t* src, const int32_t* dst, int n_copies, void* stream);
+
+/* ---------------------------------------------------------------------- */
+/* Rotary positions with several axes (time, height, width of image and    */
+/* video tokens; "Gemma 4: End-to-End Architecture Walkthrough", 2: a vision */
+/* encoder rotates one half of an embedding by x and the other by y). A     */
+/* caller that uses it passes rope_frac 0 to the attention calls.            */
+/*                                                                        */
+/* q, k [tokens][heads][head_dim] bf16 with token strides of q_stride and   */
+/*        k_stride elements (heads are dense; slices of a fused projection  */
+/*        will do); k may be NULL when n_kv_heads is 0. head_dim: a          */
+/*        multiple of 8, at most 512. Strides: multiples of 8.               */
+/* positions device int32 [n_axes][tokens], any value; n_axes 1 to 4.       */
+/* axis_pairs host int [n_axes]: how many of the dimension pairs (2i, 2i+1) */
+/*        turn with each axis, in all at most head_dim / 2; the remaining    */
+/*        pairs (the last ones) are copied.                                  */
+/* Pair i turns by positions[axis][t] * rope_theta^(-2i/head_dim).            */
+/* Outputs: written with strides of their own; an output is its input (same */
+/*        pointer and stride) or does not overlap it, nor the other one.     */
+/* flags:                                                                   */
+/*   GEMMA_ROPE_INTERLEAVED: pairs go to the axes in turn (while an axis     */
+/*        has pairs left); without it the first axis_pairs[0] pairs belong   */
+/*        to axis 0, the next ones to axis 1, and so on.                      */
+/*   GEMMA_ROPE_AXIS_LADDERS: the r-th of an axis's n pairs turns with        */
+/*        rope_theta^(-r/n): every axis has the whole range of frequencies.   */
+/*   GEMMA_ROPE_INVERSE: turns the other way: the gradient of the call        */
+/*        without it, and the way back from rotated to plain vectors.         */
+/* ---------------------------------------------------------------------- */
+#define GEMMA_ROPE_INTERLEAVED 1u
+#define GEMMA_ROPE_AXIS_LADDERS 2u
+#define GEMMA_ROPE_INVERSE 4u
+int gemma_rope_axes(const void* q, long long q_stride, const void* k, long long k_stride,
+                    const int32_t* positions, int n_axes, const int* axis_pairs, int tokens,
+                    int n_q_heads, int n_kv_heads, int head_dim, float rope_theta, void* q_out,
+                    long long q_out_stride, void* k_out, long long k_out_stride, unsigned flags,
+                    void* stream);
+
+/* ---------------------------------------------------------------------- */
 /* Decode without allocation. The pages have no counterpart for this entry */
 /* point; it exists for callers that cannot obtain device memory for the  */
 /* decode workspace -- e.g. a plugin inside a host runtime that owns all  */
@@ -408,8 +569,8 @@ const char* gemma_last_error(void);
 int gemma_attn_set_wait_limit(long long max_ns);
 
 /* Test hook for the same path: when `enable` is nonzero, the next
- * gemma_attn_decode launch (or gemma_attn_decode_multi launch of the
- * tensor-core kernel) does not issue the first key/value copy of its
+ * gemma_attn_decode or gemma_attn_decode_sinks launch (or
+ * gemma_attn_decode_multi launch of the tensor-core kernel) does not issue the first key/value copy of its
  * first work unit, so that unit's consumers wait on a barrier nothing will
  * complete; their bounded wait runs out, the unit exits without output and
  * gemma_attn_sync_status reports GEMMA_ERR_DEVICE_TIMEOUT. Nothing faults or

@@ -31,9 +31,10 @@ __host__ __device__ __forceinline__ int64_t visible_range(int64_t pos, int windo
 // Visible keys of a windowed query that also sees the sequence's first
 // `sinks` positions: the query at position len - 1 sees j < len iff
 // j >= lo (= len - window, at least 0) or j < sinks. They are walked in a
-// virtual order of whole 32-key blocks: n_sink keys from position 0, then from
-// position `start` on, n in all (the first and last block of a run may hold
-// positions that the query does not see).
+// virtual order of whole blocks of `block` keys (a power of two that divides
+// the page size): n_sink keys from position 0, then from position `start` on,
+// n in all (the first and last block of a run may hold positions that the
+// query does not see).
 struct SinkSpan {
   int lo, n_sink, start, n;
   __host__ __device__ __forceinline__ int position(int v) const { return v < n_sink ? v : start + (v - n_sink); }
@@ -42,13 +43,13 @@ struct SinkSpan {
   }
 };
 
-__host__ __device__ __forceinline__ SinkSpan sink_span(int64_t len, int window, int sinks) {
+__host__ __device__ __forceinline__ SinkSpan sink_span(int64_t len, int window, int sinks, int block) {
   SinkSpan s;
   s.lo = len > window ? (int)(len - window) : 0;
   s.n_sink = 0;
-  s.start = s.lo & ~31;
+  s.start = s.lo & ~(block - 1);
   if (sinks > 0) {
-    const int first = sinks < s.lo ? (sinks + 31) & ~31 : s.lo;  // end of the sinks' blocks
+    const int first = sinks < s.lo ? (sinks + block - 1) & ~(block - 1) : s.lo;  // end of the sinks' blocks
     if (first < s.start)
       s.n_sink = first;
     else

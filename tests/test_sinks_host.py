@@ -198,12 +198,12 @@ def test_struct_fields_match_the_header(name):
 
 
 # ------------------------------------------------------------ the decode kernel's walk
-def span(length, window, sinks):
+def span(length, window, sinks, block):
     """sink_span of csrc/common.cuh, restated: (lo, n_sink, start, n)."""
     lo = max(0, length - window)
-    n_sink, start = 0, lo // 32 * 32
+    n_sink, start = 0, lo // block * block
     if sinks > 0:
-        first = (sinks + 31) // 32 * 32 if sinks < lo else lo
+        first = -(-sinks // block) * block if sinks < lo else lo
         if first < start:
             n_sink = first
         else:
@@ -211,22 +211,23 @@ def span(length, window, sinks):
     return lo, n_sink, start, n_sink + length - start
 
 
+@pytest.mark.parametrize("block", [32, 64])
 @pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 64, 100, 1 << 30])
 @pytest.mark.parametrize("sinks", [0, 1, 31, 32, 33, 70, 300, 1 << 30])
-def test_walk_covers_every_visible_key_once(window, sinks):
+def test_walk_covers_every_visible_key_once(window, sinks, block):
     for length in [1, 2, 31, 32, 33, 64, 65, 100, 131, 200, 333, 400]:
-        lo, n_sink, start, n = span(length, window, sinks)
-        assert start % 32 == 0 and n_sink % 32 == 0 and 0 < n <= length
+        lo, n_sink, start, n = span(length, window, sinks, block)
+        assert start % block == 0 and n_sink % block == 0 and 0 < n <= length
         walked = [v if v < n_sink else start + v - n_sink for v in range(n)]
         assert len(set(walked)) == n and max(walked) == length - 1
         seen = [p for p in walked if p >= lo or p < sinks]
         assert seen == [j for j in range(length) if sees(j, length - 1, window, sinks)]
-        # whole blocks of the walk are whole 32-position blocks, each with a visible key
-        for v in range(0, n, 32):
-            block = walked[v:v + 32]
-            assert block[0] % 32 == 0 and block == list(range(block[0], block[0] + len(block)))
+        # every block of the walk is a whole block of positions; two runs only where each block has a visible key
+        for v in range(0, n, block):
+            tile = walked[v:v + block]
+            assert tile[0] % block == 0 and tile == list(range(tile[0], tile[0] + len(tile)))
             if n_sink:
-                assert any(p >= lo or p < sinks for p in block)
+                assert any(p >= lo or p < sinks for p in tile)
 
 
 def test_reference_book_and_attention_are_what_they_say():

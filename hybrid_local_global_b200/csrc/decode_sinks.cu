@@ -14,22 +14,23 @@
 //
 // Visible keys are walked in a virtual order of whole 32-key blocks: those of
 // the sinks, then those from the one that holds the window's first key on (one
-// run when the two meet); a block never straddles a page. Four blocks make a
-// tile of 128 keys. The product is taken transposed, as in the multi-token
-// kernel, so that the keys fill the MMA's 128 rows and the few q heads are its
-// columns:
+// run when the two meet). A tile is the walked blocks of 128 aligned positions
+// (so it lies in one page; the first and last of a CTA's may have fewer than
+// four). The product is taken transposed, as in the multi-token kernel, so that
+// the keys fill the MMA's 128 rows and the few q heads are its columns:
 //   S^T = K Q^T    (M = 128 keys, N = 16, K = head_dim)
 //   O^T += V^T P^T (M = 128 value dims per MMA, N = 16, K = 32 keys per block)
 // A group has at most 8 heads and N is at least 16: columns 0..7 take the bf16
 // values of Q~ (and of the weights P), columns 8..15 what that rounding lost,
 // and the two halves are added, so neither rounding shows in the result.
 //
-// CTA = 192 threads: warp 0 loads (TMA, boxes of 32 keys x 64 dims into 32 KB
-// stages of 128 keys x 128 dims), warp 1 issues the MMAs and owns TMEM, warps
-// 2..5 rotate q and the new key, run the softmax (thread = key = TMEM lane)
-// and merge. The new token's row is not read back from the cache: warp 1 puts
-// it into its tile. Rows that the query does not see are masked in S and
-// cleared in V (their weight is 0, but 0 * NaN is not).
+// CTA = 192 threads: warp 0 loads 32 KB stages of 128 keys x 128 dims (one TMA
+// copy for a whole tile's stage, boxes of 32 keys for the others), warp 1
+// issues the MMAs and owns TMEM, warps 2..5 rotate q and the new key, run the
+// softmax (thread = key = TMEM lane) and merge. The new token's row is not read
+// back from the cache: warp 1 puts it into its tile. Rows that the query does
+// not see are masked in S and cleared in V (their weight is 0, but 0 * NaN is
+// not).
 //
 // HBM-bound: every visible K/V byte is read once per KV head (under K = V
 // the second read of a row hits L2).
@@ -75,6 +76,7 @@ struct Ctl {
   int issued[NS], consumed[NS];
   float m[8], f[8], l[8];         // running maxima, rescale factors, sums (this CTA)
   float red[4][8];
+  alignas(16) float wgt[MAX_CLUSTER][8];
   float2 ml[MAX_CLUSTER][8];      // the cluster's (m, l); l < 0: that CTA gave up
 };
 
@@ -181,10 +183,44 @@ __device__ __forceinline__ void turn4(const uint4& x, int c, int n_rot, const fl
   }
 }
 
+// The tiles of a CTA's blocks [blk0, blk0 + n_blk) of the walk.
+struct Tile {
+  int i, nb, p0;  // first block, blocks, position of row 0
+};
+struct Walk {
+  SinkSpan sp;
+  int blk0, n_blk;
+  __device__ __forceinline__ Tile at(int i) const {
+    const int v = (blk0 + i) * BLK, p0 = sp.position(v);
+    int nb = min(4 - ((p0 / BLK) & 3), n_blk - i);
+    if (v < sp.n_sink) nb = min(nb, (sp.n_sink - v) / BLK);
+    return Tile{i, nb, p0};
+  }
+};
+
+// D[tmem] (+)= A[smem] * B[smem] with descriptors as (low word + offset, high word)
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                    uint32_t idesc, uint32_t accumulate) {
+  tc::mma_ss(d, (uint64_t)a_hi << 32 | a_lo, (uint64_t)b_hi << 32 | b_lo, idesc, accumulate);
+}
+
+struct Maps {
+  CUtensorMap k, v;            // boxes of 128 keys x 128 dims
+  CUtensorMap k_part, v_part;  // boxes of 32 keys x 64 dims
+};
+
+__device__ __forceinline__ void load_5d(uint32_t dst, const CUtensorMap* m, int row, int chunk, int head, int page,
+                                        uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(0), "r"(row), "r"(chunk), "r"(head), "r"(page)
+      : "memory");
+}
+
 template <int D, int CTAS>
 __global__ void __launch_bounds__(192, CTAS)
-    k_decode_sinks(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                   const __grid_constant__ SinkDecodeArgs a) {
+    k_decode_sinks(const __grid_constant__ Maps maps, const __grid_constant__ SinkDecodeArgs a) {
   using C = Cfg<D, CTAS>;
   constexpr int NS = C::NS, MT = C::MT, CH = D / 8;  // CH: 16-byte chunks of a row
   extern __shared__ unsigned char sm_raw[];
@@ -215,7 +251,7 @@ __global__ void __launch_bounds__(192, CTAS)
   const int per = (blocks + n_splits - 1) / n_splits;
   const int blk0 = min(split * per, blocks);
   const int n_blk = min(per, blocks - blk0);       // this CTA's blocks
-  const int n_tiles = (n_blk + 3) / 4;
+  const Walk walk{sp, blk0, n_blk};
   const bool own_new = has_new && n_blk > 0 && blk0 + n_blk == blocks;  // its last block holds the new token
 
   if (tid == 0) {
@@ -252,148 +288,160 @@ __global__ void __launch_bounds__(192, CTAS)
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    int page0 = -1, ent = 0;  // this lane's table entry: of page page0 + lane
-    int item = 0;
-    bool ok = true;
-    for (int j = 0; j <= n_tiles && ok; ++j) {
-      for (int kind = 0; kind < 2 && ok; ++kind) {  // 0: K_j, 1: V_{j-1}
-        if ((kind == 0 && j == n_tiles) || (kind == 1 && j == 0)) continue;
-        const int i0 = (j - kind) * 4, nb = min(4, n_blk - i0);
-        // lane's box of every stage: block lane / 2, 64-dim half lane % 2
-        int row = 0, page = 0;
-        for (int q = 0; q < nb; ++q) {
-          const int p0 = sp.position((blk0 + i0 + q) * BLK);
-          const int pi = p0 / a.page_size;
-          if (page0 < 0 || pi < page0 || pi >= page0 + 32) {
-            page0 = pi;
-            ent = pi + lane < a.pages_per_seq ? a.page_table[(int64_t)b * a.pages_per_seq + pi + lane] : 0;
+    if (lane == 0) {
+      tc::prefetch_tmap(&maps.k);
+      tc::prefetch_tmap(&maps.v);
+      tc::prefetch_tmap(&maps.k_part);
+      tc::prefetch_tmap(&maps.v_part);
+      const int32_t* table = a.page_table + (int64_t)b * a.pages_per_seq;
+      int item = 0;
+      bool ok = true;
+      const auto load = [&](const Tile& t, int page, bool isv) {
+        const CUtensorMap* whole = isv ? &maps.v : &maps.k;
+        const CUtensorMap* part = isv ? &maps.v_part : &maps.k_part;
+        const int row = t.p0 % a.page_size;
+        for (int h = 0; h < MT && ok; ++h, ++item) {
+          const int s = item % NS;
+          if (item >= NS)
+            ok = mbar_wait_bounded_at(&ctl->empty[s], ((item / NS) - 1) & 1, abort_flag, deadline, a.status, 51, item,
+                                      s, t.i);
+          if (!ok || *abort_flag) {
+            ok = false;
+            break;
           }
-          const int e = __shfl_sync(0xffffffffu, ent, pi - page0);
-          if (lane >> 1 == q) {
-            row = p0 - pi * a.page_size;
-            page = e;
+          if (a.drop_first_copy && item == 0 && split == 0 && g == 0 && b == 0) continue;
+          const uint32_t dst = base + s * STAGE_B, bar = smem_u32(&ctl->full[s]);
+          mbar_arrive_expect_tx(&ctl->full[s], (uint32_t)(t.nb * 2 * BOX_B));
+          ctl->issued[s] += 1;
+          if (t.nb == 4) {
+            load_5d(dst, whole, row, h * 2, g, page, bar);
+          } else {
+            for (int q = 0; q < t.nb; ++q) {
+              load_5d(dst + q * BOX_B, part, row + q * BLK, h * 2, g, page, bar);
+              load_5d(dst + CH_B + q * BOX_B, part, row + q * BLK, h * 2 + 1, g, page, bar);
+            }
           }
         }
+      };
+      // K_0, K_1, V_0, K_2, V_1, ...; the next tile's page is looked up a tile ahead
+      Tile t = walk.at(0);
+      int page = n_blk > 0 ? table[t.p0 / a.page_size] : 0;
+      Tile pt = t;
+      int ppage = 0;
+      for (int i = 0; i < n_blk && ok;) {
         if (page < 0 || page >= a.n_pages) {  // a page outside the pool: report it and read page 0 (finite, wrong)
           set_status(a.status, GEMMA_ERR_DEVICE_RANGE);
           page = 0;
         }
-        const CUtensorMap* map = kind == 0 ? &tm_k : &tm_v;
-        for (int h = 0; h < MT; ++h, ++item) {
-          const int s = item % NS;
-          if (lane == 0) {
-            if (item >= NS)
-              ok = mbar_wait_bounded_at(&ctl->empty[s], ((item / NS) - 1) & 1, abort_flag, deadline, a.status, 51,
-                                        item, s, j);
-            if (ok && *abort_flag) ok = false;
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) break;
-          if (a.drop_first_copy && item == 0 && split == 0 && g == 0 && b == 0) continue;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&ctl->full[s], (uint32_t)(nb * 2 * BOX_B));
-            ctl->issued[s] += 1;
-          }
-          __syncwarp();
-          if (lane < 2 * nb)
-            tc::tma_load_4d(base + s * STAGE_B + (lane & 1) * CH_B + (lane >> 1) * BOX_B, map,
-                            h * 128 + (lane & 1) * 64, row, g, page, smem_u32(&ctl->full[s]));
-        }
+        const int next = i + t.nb;
+        const Tile nt = walk.at(min(next, n_blk - 1));
+        const int npage = next < n_blk ? table[nt.p0 / a.page_size] : 0;
+        load(t, page, false);
+        if (i > 0 && ok) load(pt, ppage, true);
+        pt = t;
+        ppage = page;
+        t = nt;
+        page = npage;
+        i = next;
       }
+      if (n_blk > 0 && ok) load(pt, ppage, true);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    bool ok = n_tiles == 0 || wait_all(&ctl->q_ready, 0, abort_flag, deadline, a.status, 50, 0, 0, 0);
-    const int new_row = own_new ? ((n_blk - 1) & 3) * BLK + len_c - sp.position((blk0 + n_blk - 1) * BLK) : -1;
+    bool ok = n_blk == 0 || wait_all(&ctl->q_ready, 0, abort_flag, deadline, a.status, 50, 0, 0, 0);
+    const uint64_t dk = tc::smem_desc_sw128(base, 16, 1024), dv = tc::smem_desc_sw128(base, CH_B, 1024);
+    const uint64_t dq = tc::smem_desc_sw128(base + C::Q_OFF, 16, 1024);
+    const uint32_t k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32), q_hi = (uint32_t)(dq >> 32);
+    const uint32_t q_lo = (uint32_t)dq, p_lo = q_lo + ((C::P_OFF - C::Q_OFF) >> 4);
     int item = 0;
-    for (int j = 0; j <= n_tiles && ok; ++j) {
-      if (j < n_tiles) {
-        const uint32_t d_s = tmem + C::COL_S + (uint32_t)(j & 1) * NQ;
-        for (int h = 0; h < MT; ++h, ++item) {
-          const int s = item % NS;
-          if (!wait_all(&ctl->full[s], (item / NS) & 1, abort_flag, deadline, a.status, 52, item, s, j)) {
-            ok = false;
-            break;
-          }
-          const uint32_t st = base + s * STAGE_B;
-          if (own_new && j == n_tiles - 1) {  // the new key's row
-            if (lane < 16) {
-              const int cc = lane >> 3, u = lane & 7;
-              *reinterpret_cast<uint4*>(sm + s * STAGE_B + cc * CH_B + new_row * 128 + ((u ^ (new_row & 7)) << 4)) =
-                  *reinterpret_cast<const uint4*>(newrow + h * 128 + lane * 8);
+    // waits for the next stage; returns its number
+    const auto take = [&](int j) {
+      const int s = item % NS;
+      ok = wait_all(&ctl->full[s], (item / NS) & 1, abort_flag, deadline, a.status, 52, item, s, j);
+      ++item;
+      if (ok && lane == 0) ctl->consumed[s] += 1;
+      return s;
+    };
+    const auto values = [&](const Tile& t, int j) {  // O^T += V_j^T P_j^T
+      // rows that the query does not see, or that the new token's row fills in
+      uint32_t off[4] = {0u, 0u, 0u, 0u};
+      bool edge = false;
+      if (!(t.p0 + t.nb * BLK <= len_c && (t.p0 >= sp.lo || t.p0 + t.nb * BLK <= a.sinks))) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q < t.nb) off[q] = ~__ballot_sync(0xffffffffu, sp.sees(t.p0 + q * BLK + lane, len_c, a.sinks));
+        edge = true;
+      }
+      const int new_row = has_new && t.p0 + t.nb * BLK > len_c ? len_c - t.p0 : -1;
+      ok = wait_all(&ctl->p_ready[j & 1], (j >> 1) & 1, abort_flag, deadline, a.status, 53, j, 0, 0);
+      for (int m = 0; m < MT && ok; ++m) {
+        const int s = take(j);
+        if (!ok) break;
+        if (edge) {
+          // lane: 16-byte unit lane % 16 of every second row
+          const int cc = (lane >> 3) & 1, u = lane & 7;
+          unsigned char* st = sm + s * STAGE_B + cc * CH_B;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            for (uint32_t left = off[q] & (lane < 16 ? 0x55555555u : 0xaaaaaaaau); left; left &= left - 1) {
+              const int r = q * BLK + __ffs(left) - 1;
+              *reinterpret_cast<uint4*>(st + r * 128 + ((u ^ (r & 7)) << 4)) = make_uint4(0, 0, 0, 0);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          if (lane == 0) {
-            ctl->consumed[s] += 1;
-            tc::fence_after_sync();
-#pragma unroll
-            for (int cc = 0; cc < 2; ++cc)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc::mma_ss(d_s, tc::smem_desc_sw128(st + cc * CH_B + kk * 32, 16, 1024),
-                           tc::smem_desc_sw128(base + C::Q_OFF + (h * 2 + cc) * (NQ * 128) + kk * 32, 16, 1024),
-                           IDESC_ST, (h | cc | kk) != 0);
-            tc::commit(smem_u32(&ctl->empty[s]));
-          }
+          __syncwarp();
+          if (new_row >= 0 && lane < 16)
+            *reinterpret_cast<uint4*>(st + new_row * 128 + ((u ^ (new_row & 7)) << 4)) =
+                *reinterpret_cast<const uint4*>(newrow + (a.keqv ? 0 : D) + m * 128 + lane * 8);
+          fence_proxy_async_smem();
           __syncwarp();
         }
-        if (!ok) break;
-        if (lane == 0) tc::commit(smem_u32(&ctl->s_full[j & 1]));
+        if (lane == 0) {
+          tc::fence_after_sync();
+          // V^T: 128 dims (two 64-dim boxes CH_B apart) x 16 keys; P^T: 16 columns x 16 keys
+          const uint32_t v_lo = (uint32_t)dv + s * (STAGE_B >> 4), pj = p_lo + (j & 1) * (P_B >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            if (kk < 2 * t.nb)
+              mma(tmem + m * NQ, v_lo + kk * (2048 >> 4), v_hi, pj + (kk >> 2) * (NQ * 128 >> 4) + (kk & 3) * 2, q_hi,
+                  IDESC_OT, (j > 0 || kk) ? 1u : 0u);
+          tc::commit(smem_u32(&ctl->empty[s]));
+        }
+        __syncwarp();
       }
-      if (j >= 1) {
-        const int i0 = (j - 1) * 4, nb = min(4, n_blk - i0);
-        uint32_t edge = 0;  // blocks with rows to clear or to fill in
-        for (int q = 0; q < nb; ++q) {
-          const int p0 = sp.position((blk0 + i0 + q) * BLK);
-          if (!(p0 + BLK <= len_c && (p0 >= sp.lo || p0 + BLK <= a.sinks))) edge |= 1u << q;
-        }
-        if (!wait_all(&ctl->p_ready[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, deadline, a.status, 53, j, 0, 0)) {
-          ok = false;
-          break;
-        }
-        const uint32_t pb = base + C::P_OFF + (uint32_t)((j - 1) & 1) * P_B;
-        for (int m = 0; m < MT; ++m, ++item) {
-          const int s = item % NS;
-          if (!wait_all(&ctl->full[s], (item / NS) & 1, abort_flag, deadline, a.status, 54, item, s, j)) {
-            ok = false;
-            break;
-          }
-          const uint32_t st = base + s * STAGE_B;
-          if (edge) {
-            for (int q = 0; q < nb; ++q) {
-              if (!(edge >> q & 1)) continue;
-              const int p0 = sp.position((blk0 + i0 + q) * BLK);
-              for (int i = lane; i < BLK * 16; i += 32) {
-                const int r = i / 16, cc = (i / 8) & 1, u = i & 7;
-                const bool is_new = has_new && p0 + r == len_c;
-                if (!is_new && sp.sees(p0 + r, len_c, a.sinks)) continue;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (is_new)
-                  v = *reinterpret_cast<const uint4*>(newrow + (a.keqv ? 0 : D) + m * 128 + cc * 64 + u * 8);
-                *reinterpret_cast<uint4*>(sm + s * STAGE_B + cc * CH_B + (q * BLK + r) * 128 + ((u ^ (r & 7)) << 4)) = v;
-              }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          if (lane == 0) {
-            ctl->consumed[s] += 1;
-            tc::fence_after_sync();
-            for (int kk = 0; kk < 2 * nb; ++kk)
-              // V^T: 128 dims (two 64-dim boxes CH_B apart) x 16 keys; P^T: 16 columns x 16 keys
-              tc::mma_ss(tmem + m * NQ, tc::smem_desc_sw128(st + kk * 2048, CH_B, 1024),
-                         tc::smem_desc_sw128(pb + (kk >> 2) * (NQ * 128) + (kk & 3) * 32, 16, 1024), IDESC_OT,
-                         (j - 1 > 0 || kk) ? 1u : 0u);
-            tc::commit(smem_u32(&ctl->empty[s]));
-          }
+      if (ok && lane == 0) tc::commit(smem_u32(&ctl->o_done[j & 1]));
+    };
+    Tile t = walk.at(0), pt = t;
+    int j = 0;
+    for (int i = 0; i < n_blk && ok; i += t.nb, ++j) {
+      t = walk.at(i);
+      const int new_row = own_new && i + t.nb == n_blk ? len_c - t.p0 : -1;
+      for (int h = 0; h < MT; ++h) {  // S_j^T = K_j Q^T
+        const int s = take(j);
+        if (!ok) break;
+        if (new_row >= 0) {
+          const int cc = (lane >> 3) & 1, u = lane & 7;
+          if (lane < 16)
+            *reinterpret_cast<uint4*>(sm + s * STAGE_B + cc * CH_B + new_row * 128 + ((u ^ (new_row & 7)) << 4)) =
+                *reinterpret_cast<const uint4*>(newrow + h * 128 + lane * 8);
+          fence_proxy_async_smem();
           __syncwarp();
         }
-        if (!ok) break;
-        if (lane == 0) tc::commit(smem_u32(&ctl->o_done[(j - 1) & 1]));
+        if (lane == 0) {
+          tc::fence_after_sync();
+          const uint32_t k_lo = (uint32_t)dk + s * (STAGE_B >> 4), qh = q_lo + h * (2 * NQ * 128 >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma(tmem + C::COL_S + (j & 1) * NQ, k_lo + (kk >> 2) * (CH_B >> 4) + (kk & 3) * 2, k_hi,
+                qh + (kk >> 2) * (NQ * 128 >> 4) + (kk & 3) * 2, q_hi, IDESC_ST, (h | kk) != 0);
+          tc::commit(smem_u32(&ctl->empty[s]));
+        }
+        __syncwarp();
       }
+      if (!ok) break;
+      if (lane == 0) tc::commit(smem_u32(&ctl->s_full[j & 1]));
+      if (j > 0) values(pt, j - 1);
+      pt = t;
     }
+    if (n_blk > 0 && ok) values(pt, j - 1);
     // no MMA may be in flight when TMEM or shared memory is released
     if (lane == 0) {
       tc::commit(smem_u32(&ctl->drain));
@@ -406,7 +454,7 @@ __global__ void __launch_bounds__(192, CTAS)
     const int kl = q4 * 32 + lane;  // this thread's key of a tile = its TMEM lane
     const int t128 = tid - 64;
     const uint32_t tm = tmem + ((uint32_t)(q4 * 32) << 16);
-    if (n_tiles > 0) {
+    if (n_blk > 0) {
       // Q^T rows 0..7: heads, 8..15: their remainders; 128-byte rows of 64
       // dims, 16-byte units swizzled by the row
       uint4 x[8 * CH / 128];
@@ -462,7 +510,10 @@ __global__ void __launch_bounds__(192, CTAS)
     // for all of them.
     bool bad = false;
     int pv_seen = 0;  // PV_0 .. PV_{pv_seen-1} are known complete
-    for (int j = 0; j < n_tiles; ++j) {
+    int j = 0;
+    Tile t{0, 0, 0};
+    for (int i = 0; i < n_blk; i += t.nb, ++j) {
+      t = walk.at(i);
       if (!bad && !wait_all(&ctl->s_full[j & 1], (j >> 1) & 1, abort_flag, deadline, a.status, 56, j, 0, 0)) bad = true;
       tc::fence_after_sync();
       float v[8];
@@ -470,9 +521,7 @@ __global__ void __launch_bounds__(192, CTAS)
         uint32_t r[16];
         tmem_ld16(tm + C::COL_S + (uint32_t)(j & 1) * NQ, r);
         tc::tmem_wait_ld();
-        const int blk = j * 4 + (kl >> 5);
-        const bool seen =
-            blk < n_blk && sp.sees(sp.position((blk0 + blk) * BLK) + (kl & 31), (int)len, a.sinks);
+        const bool seen = kl < t.nb * BLK && sp.sees(t.p0 + kl, (int)len, a.sinks);
 #pragma unroll
         for (int n = 0; n < 8; ++n)
           v[n] = seen ? (__uint_as_float(r[n]) + __uint_as_float(r[n + 8])) * a.scale_log2 : -INFINITY;
@@ -546,9 +595,8 @@ __global__ void __launch_bounds__(192, CTAS)
       tc::fence_before_sync();
       mbar_arrive(&ctl->p_ready[j & 1]);
     }
-    if (!bad && n_tiles > 0)
-      bad = !wait_all(&ctl->o_done[(n_tiles - 1) & 1], ((n_tiles - 1) >> 1) & 1, abort_flag, deadline, a.status, 59,
-                      n_tiles, 0, 0);
+    if (!bad && n_blk > 0)
+      bad = !wait_all(&ctl->o_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, deadline, a.status, 59, j, 0, 0);
     good = !any128(bad);
     // sums over the tile's 128 key lanes
     const float s = reduce8<false>(l, lane);
@@ -572,29 +620,30 @@ __global__ void __launch_bounds__(192, CTAS)
   pair::cluster_sync();  // every CTA is done with its ring
   // Each CTA owns D / n_splits output columns; the others push their share of
   // those into its ring, [split][column][head], and their (m, l).
-  const int cols = D / n_splits;
+  const int log_n = __ffs(n_splits) - 1, log_cols = (D == 256 ? 8 : 9) - log_n, cols = 1 << log_cols;
   if (warp >= 2) {
     const int kl = (warp & 3) * 32 + lane;
-    if (n_tiles > 0) {
+    if (kl < n_splits * 8)
+      st_cluster2(pair::map_to(smem_u32(&ctl->ml[split][kl & 7]), kl >> 3), ctl->m[kl & 7],
+                  good ? ctl->l[kl & 7] : -1.f);
+    if (n_blk > 0) {
       tc::fence_after_sync();
       const uint32_t tm = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-#pragma unroll 1
+      uint32_t o[MT][16];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) tmem_ld16(tm + m * NQ, o[m]);
+      tc::tmem_wait_ld();
+#pragma unroll
       for (int m = 0; m < MT; ++m) {
-        uint32_t o[16];
-        tmem_ld16(tm + m * NQ, o);
-        tc::tmem_wait_ld();
         float x[8];
 #pragma unroll
-        for (int n = 0; n < 8; ++n) x[n] = __uint_as_float(o[n]) + __uint_as_float(o[n + 8]);
+        for (int n = 0; n < 8; ++n) x[n] = __uint_as_float(o[m][n]) + __uint_as_float(o[m][n + 8]);
         const int d = m * 128 + kl;
-        const uint32_t to = pair::map_to(base, d / cols) + (split * cols + d % cols) * 32;
+        const uint32_t to = pair::map_to(base, d >> log_cols) + ((split << log_cols) + (d & (cols - 1))) * 32;
         st_cluster4(to, x[0], x[1], x[2], x[3]);
         st_cluster4(to + 16, x[4], x[5], x[6], x[7]);
       }
     }
-    if (kl < n_splits * 8)
-      st_cluster2(pair::map_to(smem_u32(&ctl->ml[split][kl & 7]), kl >> 3), ctl->m[kl & 7],
-                  good ? ctl->l[kl & 7] : -1.f);
   }
   tc::fence_before_sync();
   __syncwarp();
@@ -603,28 +652,46 @@ __global__ void __launch_bounds__(192, CTAS)
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, C::TMEM_COLS);
   }
-  for (int i = tid; i < 8 * cols; i += 192) {
-    const int n = i / cols, d = i % cols;
-    if (n >= G) break;
-    float M = -INFINITY;
-    for (int s = 0; s < n_splits; ++s) M = fmaxf(M, ctl->ml[s][n].x);
-    float L = 0.f, x = 0.f;
+  // weight of each split's share, 2^(m_s - M) / L (thread: head tid % 8 of split tid / 8)
+  if (tid < n_splits * 8) {
+    const int n = tid & 7;
+    float M = -INFINITY, L = 0.f;
     bool ok = true;
+    for (int s = 0; s < n_splits; ++s) M = fmaxf(M, ctl->ml[s][n].x);
     for (int s = 0; s < n_splits; ++s) {
       const float2 ml = ctl->ml[s][n];
       ok = ok && !(ml.y < 0.f);
-      if (ml.x == -INFINITY) continue;  // no keys there, and no O
-      const float w = tc::ex2(ml.x - M);
-      L += w * ml.y;
-      x += w * *reinterpret_cast<const float*>(sm + ((s * cols + d) * 8 + n) * 4);
+      if (ml.x != -INFINITY) L += tc::ex2(ml.x - M) * ml.y;
     }
-    if (ok) a.out[(head0 + n) * D + split * cols + d] = __float2bfloat16_rn(x / L);
+    const float m = ctl->ml[tid >> 3][n].x;
+    ctl->wgt[tid >> 3][n] = m == -INFINITY ? 0.f : tc::ex2(m - M) / L;
+    if (!ok) ctl->abort = 1;  // some CTA gave up: no output
+  }
+  __syncthreads();
+  if (*abort_flag) return;
+  for (int i = tid; i < 2 * cols; i += 192) {  // (heads 4 hh .. 4 hh + 3, column d)
+    const int hh = i >> log_cols, d = i & (cols - 1);
+    if (4 * hh >= G) break;
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < n_splits; ++s) {
+      const float4 w = *reinterpret_cast<const float4*>(&ctl->wgt[s][4 * hh]);
+      const float4 v = *reinterpret_cast<const float4*>(sm + ((s << log_cols) + d) * 32 + hh * 16);
+      // a split without keys pushed nothing
+      if (ctl->ml[s][4 * hh].x == -INFINITY) continue;
+      x[0] += w.x * v.x;
+      x[1] += w.y * v.y;
+      x[2] += w.z * v.z;
+      x[3] += w.w * v.w;
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+      if (4 * hh + n < G)
+        a.out[(head0 + 4 * hh + n) * D + (split << log_cols) + d] = __float2bfloat16_rn(x[n]);
   }
 }
 
 template <int D, int CTAS>
-cudaError_t launch_as(const CUtensorMap& mk, const CUtensorMap& mv, const SinkDecodeArgs& a, int B, int n_splits,
-                      cudaStream_t st) {
+cudaError_t launch_as(const Maps& maps, const SinkDecodeArgs& a, int B, int n_splits, cudaStream_t st) {
   using C = Cfg<D, CTAS>;
   cudaError_t e = cudaFuncSetAttribute(k_decode_sinks<D, CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
@@ -640,7 +707,7 @@ cudaError_t launch_as(const CUtensorMap& mk, const CUtensorMap& mv, const SinkDe
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_decode_sinks<D, CTAS>, mk, mv, a);
+  return cudaLaunchKernelEx(&cfg, k_decode_sinks<D, CTAS>, maps, a);
 }
 
 // Splits per (sequence, KV head): the power of two up to MAX_CLUSTER that
@@ -665,16 +732,25 @@ int plan_splits(int B, int Hkv, int window, int sinks, int max_len) {
 
 cudaError_t launch_decode_sinks(SinkDecodeArgs& a, int B, int D, double log2_theta, cudaStream_t st) {
   for (int i = 0; i < a.n_rot; ++i) a.freq[i] = std::exp2(-(2.0 * i / D) * log2_theta) * kInvPi;
+  // (64 dims, row, 64-dim chunk, head, page): a box of 2 chunks is a stage
   const uint64_t ps = (uint64_t)a.page_size, H = (uint64_t)a.Hkv, d = (uint64_t)D;
-  const uint64_t dims[4] = {d, ps, H, (uint64_t)a.n_pages}, str[3] = {d * 2, ps * d * 2, H * ps * d * 2};
-  const uint32_t box[4] = {64, BLK, 1, 1};
-  CUtensorMap mk, mv;
-  if (!make_map_bf16_4d(&mk, a.k_pool, dims, str, box) || !make_map_bf16_4d(&mv, a.v_pool, dims, str, box))
+  const uint64_t dims[5] = {64, ps, d / 64, H, (uint64_t)a.n_pages};
+  const uint64_t str[4] = {d * 2, 128, ps * d * 2, H * ps * d * 2};
+  const uint32_t whole[5] = {64, BN, 2, 1, 1}, part[5] = {64, BLK, 1, 1, 1};
+  Maps maps;
+  if (!make_map_bf16_5d(&maps.k, a.k_pool, dims, str, whole) || !make_map_bf16_5d(&maps.k_part, a.k_pool, dims, str, part))
     return cudaErrorInvalidValue;
+  if (a.keqv) {
+    maps.v = maps.k;
+    maps.v_part = maps.k_part;
+  } else if (!make_map_bf16_5d(&maps.v, a.v_pool, dims, str, whole) ||
+             !make_map_bf16_5d(&maps.v_part, a.v_pool, dims, str, part)) {
+    return cudaErrorInvalidValue;
+  }
   const int n = plan_splits(B, a.Hkv, a.window, a.sinks, a.max_len);
   const bool deep = (int64_t)B * a.Hkv * n <= multiprocessors();
-  if (D == 256) return deep ? launch_as<256, 1>(mk, mv, a, B, n, st) : launch_as<256, 2>(mk, mv, a, B, n, st);
-  return deep ? launch_as<512, 1>(mk, mv, a, B, n, st) : launch_as<512, 2>(mk, mv, a, B, n, st);
+  if (D == 256) return deep ? launch_as<256, 1>(maps, a, B, n, st) : launch_as<256, 2>(maps, a, B, n, st);
+  return deep ? launch_as<512, 1>(maps, a, B, n, st) : launch_as<512, 2>(maps, a, B, n, st);
 }
 
 }  // namespace hlg

@@ -22,15 +22,20 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-bool make_map_4d(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, const uint64_t dims[4],
-                 const uint64_t strides[3], const uint32_t box[4]) {
+template <int N>
+bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, const uint64_t* dims,
+              const uint64_t* strides, const uint32_t* box) {
   auto fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t gd[4] = {dims[0], dims[1], dims[2], dims[3]};
-  cuuint64_t gs[3] = {strides[0], strides[1], strides[2]};
-  cuuint32_t bx[4] = {box[0], box[1], box[2], box[3]};
-  cuuint32_t es[4] = {1, 1, 1, 1};
-  CUresult r = fn(m, type, 4, const_cast<void*>(ptr), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  cuuint64_t gd[N], gs[N - 1];
+  cuuint32_t bx[N], es[N];
+  for (int i = 0; i < N; ++i) {
+    gd[i] = dims[i];
+    bx[i] = box[i];
+    es[i] = 1;
+    if (i < N - 1) gs[i] = strides[i];
+  }
+  CUresult r = fn(m, type, N, const_cast<void*>(ptr), gd, gs, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
@@ -40,12 +45,17 @@ bool make_map_4d(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, cons
 
 bool make_map_bf16_4d(CUtensorMap* m, const void* ptr, const uint64_t dims[4], const uint64_t strides[3],
                       const uint32_t box[4]) {
-  return make_map_4d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, dims, strides, box);
+  return make_map<4>(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, dims, strides, box);
+}
+
+bool make_map_bf16_5d(CUtensorMap* m, const void* ptr, const uint64_t dims[5], const uint64_t strides[4],
+                      const uint32_t box[5]) {
+  return make_map<5>(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, dims, strides, box);
 }
 
 bool make_map_u8_4d(CUtensorMap* m, const void* ptr, const uint64_t dims[4], const uint64_t strides[3],
                     const uint32_t box[4]) {
-  return make_map_4d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, ptr, dims, strides, box);
+  return make_map<4>(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, ptr, dims, strides, box);
 }
 
 bool make_prefill_maps(const PrefillAttnArgs& a, int B, int D, int key_rows_total, int kv_token_major,

@@ -1,4 +1,4 @@
-// tmap.h -- host-side TMA tensor maps (prefill attention, int8 decode).
+// tmap.h -- host-side TMA tensor maps (prefill attention, int8 and windowed decode).
 #pragma once
 
 #include <cuda.h>
@@ -13,7 +13,10 @@ namespace hlg {
 // the driver entry point is missing or rejects the layout.
 bool make_map_bf16_4d(CUtensorMap* m, const void* ptr, const uint64_t dims[4], const uint64_t strides[3],
                       const uint32_t box[4]);
-// The same for a uint8 tensor (int8 KV codes); box[0] <= 128 bytes.
+// The same with five dimensions.
+bool make_map_bf16_5d(CUtensorMap* m, const void* ptr, const uint64_t dims[5], const uint64_t strides[4],
+                      const uint32_t box[5]);
+// The 4-D map for a uint8 tensor (int8 KV codes); box[0] <= 128 bytes.
 bool make_map_u8_4d(CUtensorMap* m, const void* ptr, const uint64_t dims[4], const uint64_t strides[3],
                     const uint32_t box[4]);
 

@@ -24,13 +24,13 @@
 // values of Q~ (and of the weights P), columns 8..15 what that rounding lost,
 // and the two halves are added, so neither rounding shows in the result.
 //
-// CTA = 192 threads: warp 0 loads 32 KB stages of 128 keys x 128 dims (one TMA
+// CTA = 224 threads: warp 0 loads 32 KB stages of 128 keys x 128 dims (one TMA
 // copy for a whole tile's stage, boxes of 32 keys for the others), warp 1
-// issues the MMAs and owns TMEM, warps 2..5 rotate q and the new key, run the
-// softmax (thread = key = TMEM lane) and merge. The new token's row is not read
-// back from the cache: warp 1 puts it into its tile. Rows that the query does
-// not see are masked in S and cleared in V (their weight is 0, but 0 * NaN is
-// not).
+// issues the MMAs (one lane) and owns TMEM, warps 2..5 rotate q and the new key,
+// run the softmax (thread = key = TMEM lane) and merge. Warp 6 puts the stages
+// of edge tiles in order before their MMAs: the new token's row, which is not
+// read back from the cache, and zeros in the rows of V that the query does not
+// see (they are masked in S and their weight is 0, but 0 * NaN is not).
 //
 // HBM-bound: every visible K/V byte is read once per KV head (under K = V
 // the second read of a row hits L2).
@@ -54,6 +54,7 @@ namespace {
 
 constexpr int BLK = 32;             // keys per block of the walk
 constexpr int BN = 128;             // keys per tile
+constexpr int NT = 224;             // threads
 constexpr int NQ = 16;              // MMA columns: 8 heads, then 8 remainders
 constexpr int CH_B = BN * 128;      // [128 keys][64 dims], swizzled
 constexpr int STAGE_B = 2 * CH_B;   // 128 dims of a K or V tile
@@ -68,12 +69,14 @@ constexpr uint32_t IDESC_OT = tc::idesc_bf16_f32(128, NQ, 1, 0);  // V^T (MN-maj
 template <int NS>
 struct Ctl {
   uint64_t full[NS], empty[NS];
+  uint64_t patch_req;             // the issuer has come to the next stages that need warp 6
+  uint64_t patched[NS];           // and their rows are in order
   uint64_t q_ready;               // 128 softmax threads: Q and the new rows are staged
   uint64_t s_full[2], p_ready[2], o_done[2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
-  int issued[NS], consumed[NS];
+  int issued, taken;              // stages loaded, stages whose load was waited for
   float m[8], f[8], l[8];         // running maxima, rescale factors, sums (this CTA)
   float red[4][8];
   alignas(16) float wgt[MAX_CLUSTER][8];
@@ -183,18 +186,35 @@ __device__ __forceinline__ void turn4(const uint4& x, int c, int n_rot, const fl
   }
 }
 
-// The tiles of a CTA's blocks [blk0, blk0 + n_blk) of the walk.
+// The tiles of a CTA's blocks [blk0, blk0 + n_blk) of the walk: the walked
+// blocks of 128 aligned positions (one page), or all of them when there are at
+// most four (whatever their positions: a short split is one tile).
 struct Tile {
   int i, nb, p0;  // first block, blocks, position of row 0
 };
 struct Walk {
   SinkSpan sp;
   int blk0, n_blk;
+  __device__ __forceinline__ int block_pos(int i) const { return sp.position((blk0 + i) * BLK); }
   __device__ __forceinline__ Tile at(int i) const {
     const int v = (blk0 + i) * BLK, p0 = sp.position(v);
-    int nb = min(4 - ((p0 / BLK) & 3), n_blk - i);
-    if (v < sp.n_sink) nb = min(nb, (sp.n_sink - v) / BLK);
+    int nb = n_blk - i;
+    if (n_blk > 4) {
+      nb = min(nb, 4 - ((p0 / BLK) & 3));
+      if (v < sp.n_sink) nb = min(nb, (sp.n_sink - v) / BLK);
+    }
     return Tile{i, nb, p0};
+  }
+  // Blocks of t (bits) with rows that the query does not see among the first
+  // len_c positions of the sequence (the new token's row included).
+  __device__ __forceinline__ uint32_t edges(const Tile& t, int len_c, int sinks) const {
+    uint32_t e = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int p = block_pos(t.i + q);
+      if (q < t.nb && !(p + BLK <= len_c && (p >= sp.lo || p + BLK <= sinks))) e |= 1u << q;
+    }
+    return e;
   }
 };
 
@@ -219,7 +239,7 @@ __device__ __forceinline__ void load_5d(uint32_t dst, const CUtensorMap* m, int 
 }
 
 template <int D, int CTAS>
-__global__ void __launch_bounds__(192, CTAS)
+__global__ void __launch_bounds__(NT, CTAS)
     k_decode_sinks(const __grid_constant__ Maps maps, const __grid_constant__ SinkDecodeArgs a) {
   using C = Cfg<D, CTAS>;
   constexpr int NS = C::NS, MT = C::MT, CH = D / 8;  // CH: 16-byte chunks of a row
@@ -240,7 +260,7 @@ __global__ void __launch_bounds__(192, CTAS)
   if (len < 1 || len > a.max_len) {  // an idle slot (0) or a bad length: zeros; the whole cluster leaves here
     if (len != 0 && tid == 0 && split == 0 && g == 0) set_status(a.status, GEMMA_ERR_DEVICE_RANGE);
     if (split == 0)
-      for (int i = tid; i < G * CH; i += 192)
+      for (int i = tid; i < G * CH; i += NT)
         *reinterpret_cast<uint4*>(a.out + head0 * D + i * 8) = make_uint4(0, 0, 0, 0);
     return;
   }
@@ -258,16 +278,17 @@ __global__ void __launch_bounds__(192, CTAS)
     for (int s = 0; s < NS; ++s) {
       mbar_init(&ctl->full[s], 1);
       mbar_init(&ctl->empty[s], 1);
-      ctl->issued[s] = ctl->consumed[s] = 0;
+      mbar_init(&ctl->patched[s], 1);
     }
     mbar_init(&ctl->q_ready, 128);
+    mbar_init(&ctl->patch_req, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->s_full[i], 1);
       mbar_init(&ctl->p_ready[i], 128);
       mbar_init(&ctl->o_done[i], 1);
     }
     mbar_init(&ctl->drain, 1);
-    ctl->abort = 0;
+    ctl->abort = ctl->issued = ctl->taken = 0;
     fence_barrier_init();
   }
   if (tid < 8) ctl->m[tid] = -INFINITY;
@@ -296,10 +317,29 @@ __global__ void __launch_bounds__(192, CTAS)
       const int32_t* table = a.page_table + (int64_t)b * a.pages_per_seq;
       int item = 0;
       bool ok = true;
+      const auto page_of = [&](int p0) {
+        int page = table[p0 / a.page_size];
+        if (page < 0 || page >= a.n_pages) {  // a page outside the pool: report it and read page 0 (finite, wrong)
+          set_status(a.status, GEMMA_ERR_DEVICE_RANGE);
+          page = 0;
+        }
+        return page;
+      };
       const auto load = [&](const Tile& t, int page, bool isv) {
         const CUtensorMap* whole = isv ? &maps.v : &maps.k;
         const CUtensorMap* part = isv ? &maps.v_part : &maps.k_part;
         const int row = t.p0 % a.page_size;
+        const bool one = t.nb == 4 && t.p0 % BN == 0 && walk.block_pos(t.i + 3) == t.p0 + 3 * BLK;
+        int prow[4] = {row, 0, 0, 0}, ppage[4] = {page, 0, 0, 0};
+        if (!one) {
+#pragma unroll
+          for (int q = 1; q < 4; ++q)
+            if (q < t.nb) {
+              const int p = walk.block_pos(t.i + q);
+              prow[q] = p % a.page_size;
+              ppage[q] = p / a.page_size == t.p0 / a.page_size ? page : page_of(p);
+            }
+        }
         for (int h = 0; h < MT && ok; ++h, ++item) {
           const int s = item % NS;
           if (item >= NS)
@@ -312,30 +352,26 @@ __global__ void __launch_bounds__(192, CTAS)
           if (a.drop_first_copy && item == 0 && split == 0 && g == 0 && b == 0) continue;
           const uint32_t dst = base + s * STAGE_B, bar = smem_u32(&ctl->full[s]);
           mbar_arrive_expect_tx(&ctl->full[s], (uint32_t)(t.nb * 2 * BOX_B));
-          ctl->issued[s] += 1;
-          if (t.nb == 4) {
+          ctl->issued = item + 1;
+          if (one) {
             load_5d(dst, whole, row, h * 2, g, page, bar);
           } else {
-            for (int q = 0; q < t.nb; ++q) {
-              load_5d(dst + q * BOX_B, part, row + q * BLK, h * 2, g, page, bar);
-              load_5d(dst + CH_B + q * BOX_B, part, row + q * BLK, h * 2 + 1, g, page, bar);
-            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (q < t.nb) {
+                load_5d(dst + q * BOX_B, part, prow[q], h * 2, g, ppage[q], bar);
+                load_5d(dst + CH_B + q * BOX_B, part, prow[q], h * 2 + 1, g, ppage[q], bar);
+              }
           }
         }
       };
-      // K_0, K_1, V_0, K_2, V_1, ...; the next tile's page is looked up a tile ahead
-      Tile t = walk.at(0);
-      int page = n_blk > 0 ? table[t.p0 / a.page_size] : 0;
-      Tile pt = t;
-      int ppage = 0;
+      // K_0, K_1, V_0, K_2, V_1, ...; the next tile's table entry is read a tile ahead
+      Tile t = walk.at(0), pt = t;
+      int page = n_blk > 0 ? page_of(t.p0) : 0, ppage = 0;
       for (int i = 0; i < n_blk && ok;) {
-        if (page < 0 || page >= a.n_pages) {  // a page outside the pool: report it and read page 0 (finite, wrong)
-          set_status(a.status, GEMMA_ERR_DEVICE_RANGE);
-          page = 0;
-        }
         const int next = i + t.nb;
         const Tile nt = walk.at(min(next, n_blk - 1));
-        const int npage = next < n_blk ? table[nt.p0 / a.page_size] : 0;
+        const int npage = next < n_blk ? page_of(nt.p0) : 0;
         load(t, page, false);
         if (i > 0 && ok) load(pt, ppage, true);
         pt = t;
@@ -348,56 +384,37 @@ __global__ void __launch_bounds__(192, CTAS)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    bool ok = n_blk == 0 || wait_all(&ctl->q_ready, 0, abort_flag, deadline, a.status, 50, 0, 0, 0);
-    const uint64_t dk = tc::smem_desc_sw128(base, 16, 1024), dv = tc::smem_desc_sw128(base, CH_B, 1024);
-    const uint64_t dq = tc::smem_desc_sw128(base + C::Q_OFF, 16, 1024);
-    const uint32_t k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32), q_hi = (uint32_t)(dq >> 32);
-    const uint32_t q_lo = (uint32_t)dq, p_lo = q_lo + ((C::P_OFF - C::Q_OFF) >> 4);
-    int item = 0;
-    // waits for the next stage; returns its number
-    const auto take = [&](int j) {
-      const int s = item % NS;
-      ok = wait_all(&ctl->full[s], (item / NS) & 1, abort_flag, deadline, a.status, 52, item, s, j);
-      ++item;
-      if (ok && lane == 0) ctl->consumed[s] += 1;
-      return s;
-    };
-    const auto values = [&](const Tile& t, int j) {  // O^T += V_j^T P_j^T
-      // rows that the query does not see, or that the new token's row fills in
-      uint32_t off[4] = {0u, 0u, 0u, 0u};
-      bool edge = false;
-      if (!(t.p0 + t.nb * BLK <= len_c && (t.p0 >= sp.lo || t.p0 + t.nb * BLK <= a.sinks))) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (q < t.nb) off[q] = ~__ballot_sync(0xffffffffu, sp.sees(t.p0 + q * BLK + lane, len_c, a.sinks));
-        edge = true;
-      }
-      const int new_row = has_new && t.p0 + t.nb * BLK > len_c ? len_c - t.p0 : -1;
-      ok = wait_all(&ctl->p_ready[j & 1], (j >> 1) & 1, abort_flag, deadline, a.status, 53, j, 0, 0);
-      for (int m = 0; m < MT && ok; ++m) {
-        const int s = take(j);
-        if (!ok) break;
-        if (edge) {
-          // lane: 16-byte unit lane % 16 of every second row
-          const int cc = (lane >> 3) & 1, u = lane & 7;
-          unsigned char* st = sm + s * STAGE_B + cc * CH_B;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            for (uint32_t left = off[q] & (lane < 16 ? 0x55555555u : 0xaaaaaaaau); left; left &= left - 1) {
-              const int r = q * BLK + __ffs(left) - 1;
-              *reinterpret_cast<uint4*>(st + r * 128 + ((u ^ (r & 7)) << 4)) = make_uint4(0, 0, 0, 0);
-            }
-          __syncwarp();
-          if (new_row >= 0 && lane < 16)
-            *reinterpret_cast<uint4*>(st + new_row * 128 + ((u ^ (new_row & 7)) << 4)) =
-                *reinterpret_cast<const uint4*>(newrow + (a.keqv ? 0 : D) + m * 128 + lane * 8);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        if (lane == 0) {
-          tc::fence_after_sync();
+    if (lane == 0) {
+      bool ok = n_blk == 0 ||
+                mbar_wait_bounded_at(&ctl->q_ready, 0, abort_flag, deadline, a.status, 50, 0, 0, 0);
+      const uint64_t dk = tc::smem_desc_sw128(base, 16, 1024), dv = tc::smem_desc_sw128(base, CH_B, 1024);
+      const uint64_t dq = tc::smem_desc_sw128(base + C::Q_OFF, 16, 1024);
+      const uint32_t k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32), q_hi = (uint32_t)(dq >> 32);
+      const uint32_t q_lo = (uint32_t)dq, p_lo = q_lo + ((C::P_OFF - C::Q_OFF) >> 4);
+      int item = 0, taken = 0;
+      uint32_t patches = 0;  // parity of each slot's next patch
+      // waits for the next stage (and its patch); returns its slot
+      const auto take = [&](bool patch) {
+        const int s = item % NS;
+        uint64_t* bar = patch ? &ctl->patched[s] : &ctl->full[s];
+        const uint32_t parity = patch ? patches >> s & 1u : (uint32_t)(item / NS) & 1u;
+        ok = mbar_wait_bounded_at(bar, parity, abort_flag, deadline, a.status, 52, item, s, patch);
+        if (patch) patches ^= 1u << s;
+        tc::fence_after_sync();
+        ++item;
+        if (ok) taken = item;
+        return s;
+      };
+      const auto values = [&](const Tile& t, int j) {  // O^T += V_j^T P_j^T
+        const bool patch = walk.edges(t, len_c, a.sinks) != 0;
+        if (patch) mbar_arrive(&ctl->patch_req);
+        ok = mbar_wait_bounded_at(&ctl->p_ready[j & 1], (j >> 1) & 1, abort_flag, deadline, a.status, 53, j, 0, 0);
+        const uint32_t pj = p_lo + (j & 1) * (P_B >> 4);
+        for (int m = 0; m < MT && ok; ++m) {
+          const int s = take(patch);
+          if (!ok) break;
           // V^T: 128 dims (two 64-dim boxes CH_B apart) x 16 keys; P^T: 16 columns x 16 keys
-          const uint32_t v_lo = (uint32_t)dv + s * (STAGE_B >> 4), pj = p_lo + (j & 1) * (P_B >> 4);
+          const uint32_t v_lo = (uint32_t)dv + s * (STAGE_B >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             if (kk < 2 * t.nb)
@@ -405,28 +422,17 @@ __global__ void __launch_bounds__(192, CTAS)
                   IDESC_OT, (j > 0 || kk) ? 1u : 0u);
           tc::commit(smem_u32(&ctl->empty[s]));
         }
-        __syncwarp();
-      }
-      if (ok && lane == 0) tc::commit(smem_u32(&ctl->o_done[j & 1]));
-    };
-    Tile t = walk.at(0), pt = t;
-    int j = 0;
-    for (int i = 0; i < n_blk && ok; i += t.nb, ++j) {
-      t = walk.at(i);
-      const int new_row = own_new && i + t.nb == n_blk ? len_c - t.p0 : -1;
-      for (int h = 0; h < MT; ++h) {  // S_j^T = K_j Q^T
-        const int s = take(j);
-        if (!ok) break;
-        if (new_row >= 0) {
-          const int cc = (lane >> 3) & 1, u = lane & 7;
-          if (lane < 16)
-            *reinterpret_cast<uint4*>(sm + s * STAGE_B + cc * CH_B + new_row * 128 + ((u ^ (new_row & 7)) << 4)) =
-                *reinterpret_cast<const uint4*>(newrow + h * 128 + lane * 8);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        if (lane == 0) {
-          tc::fence_after_sync();
+        if (ok) tc::commit(smem_u32(&ctl->o_done[j & 1]));
+      };
+      Tile t = walk.at(0), pt = t;
+      int j = 0;
+      for (int i = 0; i < n_blk && ok; i += t.nb, ++j) {
+        t = walk.at(i);
+        const bool patch = own_new && i + t.nb == n_blk;
+        if (patch) mbar_arrive(&ctl->patch_req);
+        for (int h = 0; h < MT; ++h) {  // S_j^T = K_j Q^T
+          const int s = take(patch);
+          if (!ok) break;
           const uint32_t k_lo = (uint32_t)dk + s * (STAGE_B >> 4), qh = q_lo + h * (2 * NQ * 128 >> 4);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
@@ -434,20 +440,76 @@ __global__ void __launch_bounds__(192, CTAS)
                 qh + (kk >> 2) * (NQ * 128 >> 4) + (kk & 3) * 2, q_hi, IDESC_ST, (h | kk) != 0);
           tc::commit(smem_u32(&ctl->empty[s]));
         }
-        __syncwarp();
+        if (!ok) break;
+        tc::commit(smem_u32(&ctl->s_full[j & 1]));
+        if (j > 0) values(pt, j - 1);
+        pt = t;
       }
-      if (!ok) break;
-      if (lane == 0) tc::commit(smem_u32(&ctl->s_full[j & 1]));
-      if (j > 0) values(pt, j - 1);
-      pt = t;
-    }
-    if (n_blk > 0 && ok) values(pt, j - 1);
-    // no MMA may be in flight when TMEM or shared memory is released
-    if (lane == 0) {
+      if (n_blk > 0 && ok) values(pt, j - 1);
+      ctl->taken = taken;
+      // no MMA may be in flight when TMEM or shared memory is released
       tc::commit(smem_u32(&ctl->drain));
       volatile int never = 0;
       mbar_wait_bounded_at(&ctl->drain, 0, &never, globaltimer_ns() + 200000000ull, a.status, 55, 0, 0, 0);
     }
+  } else if (warp == 6) {
+    // ------------------------------------------------------------ edge rows
+    // Same order of stages as the issuer's, which asks for each group of MT
+    // that needs this warp once it has waited for all stages before it: the
+    // parity waits here cannot mistake an older phase for the stage's own.
+    // lane: 16-byte unit lane % 16 (of the 128 dims) of every second row.
+    bool ok = n_blk == 0 || wait_all(&ctl->q_ready, 0, abort_flag, deadline, a.status, 61, 0, 0, 0);
+    const int cc = (lane >> 3) & 1, u = lane & 7;
+    int item = 0, groups = 0;
+    // rows of t to clear (V), then the new token's row
+    const auto patch = [&](const Tile& t, bool isv) {
+      const uint32_t edge = isv ? walk.edges(t, len_c, a.sinks) : 0u;
+      const bool with_new = own_new && t.i + t.nb == n_blk;
+      if (!edge && !with_new) {
+        item += MT;
+        return;
+      }
+      ok = wait_all(&ctl->patch_req, groups++ & 1, abort_flag, deadline, a.status, 63, t.i, 0, 0);
+      uint32_t off[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        off[q] = ~__ballot_sync(0xffffffffu, !(edge >> q & 1) ||
+                                                 sp.sees(walk.block_pos(t.i + q) + lane, len_c, a.sinks));
+      const int new_row = (t.nb - 1) * BLK + len_c - walk.block_pos(t.i + t.nb - 1);
+      for (int h = 0; h < MT && ok; ++h, ++item) {
+        const int s = item % NS;
+        ok = wait_all(&ctl->full[s], (item / NS) & 1, abort_flag, deadline, a.status, 62, item, s, t.i);
+        if (!ok) break;
+        unsigned char* st = sm + s * STAGE_B + cc * CH_B;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (!(off[q] >> (16 * half) & 0xffffu)) continue;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int r = half * 16 + 2 * k + (lane >> 4);
+              if (off[q] >> r & 1u)
+                *reinterpret_cast<uint4*>(st + (q * BLK + r) * 128 + ((u ^ (r & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+            }
+          }
+        __syncwarp();
+        if (with_new && lane < 16)
+          *reinterpret_cast<uint4*>(st + new_row * 128 + ((u ^ (new_row & 7)) << 4)) =
+              *reinterpret_cast<const uint4*>(newrow + (isv && !a.keqv ? D : 0) + h * 128 + lane * 8);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->patched[s]);
+      }
+    };
+    Tile t = walk.at(0), pt = t;
+    for (int i = 0; i < n_blk && ok; i += t.nb) {
+      t = walk.at(i);
+      patch(t, false);
+      if (i > 0 && ok) patch(pt, true);
+      pt = t;
+    }
+    if (n_blk > 0 && ok) patch(pt, true);
   } else {
     // ------------------------------------------------------------ rotation, softmax
     const int q4 = warp & 3;
@@ -521,7 +583,7 @@ __global__ void __launch_bounds__(192, CTAS)
         uint32_t r[16];
         tmem_ld16(tm + C::COL_S + (uint32_t)(j & 1) * NQ, r);
         tc::tmem_wait_ld();
-        const bool seen = kl < t.nb * BLK && sp.sees(t.p0 + kl, (int)len, a.sinks);
+        const bool seen = kl < t.nb * BLK && sp.sees(walk.block_pos(t.i + (kl >> 5)) + (kl & 31), (int)len, a.sinks);
 #pragma unroll
         for (int n = 0; n < 8; ++n)
           v[n] = seen ? (__uint_as_float(r[n]) + __uint_as_float(r[n + 8])) * a.scale_log2 : -INFINITY;
@@ -529,7 +591,7 @@ __global__ void __launch_bounds__(192, CTAS)
       bool need = bad;
 #pragma unroll
       for (int n = 0; n < 8; ++n) need |= v[n] > ctl->m[n] + RESCALE_LOG2;
-      if (any128(need)) {
+      if (j == 0 || any128(need)) {
         // some logit exceeds its head's running max by more than 2^8 (or a
         // wait failed): the tile's maxima, and thread n moves head n's
         if (any128(bad)) break;
@@ -608,20 +670,19 @@ __global__ void __launch_bounds__(192, CTAS)
   __syncwarp();
   __syncthreads();
   if (warp == 0 && lane == 0 && *abort_flag) {
-    // loads still in flight must land before shared memory is reused
+    // loads still in flight must land before shared memory is reused (a
+    // dropped copy, the test hook's, never does: its wait runs out)
     volatile int never = 0;
     const uint64_t dl = globaltimer_ns() + 200000000ull;
-    for (int s = 0; s < NS; ++s)
-      if (ctl->issued[s] > ctl->consumed[s])
-        mbar_wait_bounded_at(&ctl->full[s], (ctl->issued[s] - 1) & 1, &never, dl, a.status, 60, ctl->issued[s], s,
-                             ctl->consumed[s]);
+    for (int i = ctl->taken; i < ctl->issued; ++i)
+      mbar_wait_bounded_at(&ctl->full[i % NS], (i / NS) & 1, &never, dl, a.status, 60, i, i % NS, ctl->taken);
   }
   __syncwarp();
   pair::cluster_sync();  // every CTA is done with its ring
   // Each CTA owns D / n_splits output columns; the others push their share of
   // those into its ring, [split][column][head], and their (m, l).
   const int log_n = __ffs(n_splits) - 1, log_cols = (D == 256 ? 8 : 9) - log_n, cols = 1 << log_cols;
-  if (warp >= 2) {
+  if (warp >= 2 && warp < 6) {
     const int kl = (warp & 3) * 32 + lane;
     if (kl < n_splits * 8)
       st_cluster2(pair::map_to(smem_u32(&ctl->ml[split][kl & 7]), kl >> 3), ctl->m[kl & 7],
@@ -669,7 +730,7 @@ __global__ void __launch_bounds__(192, CTAS)
   }
   __syncthreads();
   if (*abort_flag) return;
-  for (int i = tid; i < 2 * cols; i += 192) {  // (heads 4 hh .. 4 hh + 3, column d)
+  for (int i = tid; i < 2 * cols; i += NT) {  // (heads 4 hh .. 4 hh + 3, column d)
     const int hh = i >> log_cols, d = i & (cols - 1);
     if (4 * hh >= G) break;
     float x[4] = {0.f, 0.f, 0.f, 0.f};
@@ -697,7 +758,7 @@ cudaError_t launch_as(const Maps& maps, const SinkDecodeArgs& a, int B, int n_sp
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(n_splits, a.Hkv, B);
-  cfg.blockDim = dim3(192);
+  cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute at[1];

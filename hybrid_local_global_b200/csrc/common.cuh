@@ -30,32 +30,39 @@ __host__ __device__ __forceinline__ int64_t visible_range(int64_t pos, int windo
 
 // Visible keys of a windowed query that also sees the sequence's first
 // `sinks` positions: the query at position len - 1 sees j < len iff
-// j >= lo (= len - window, at least 0) or j < sinks. They are walked in a
-// virtual order of whole blocks of `block` keys (a power of two that divides
-// the page size): n_sink keys from position 0, then from position `start` on,
-// n in all (the first and last block of a run may hold positions that the
-// query does not see).
+// j >= lo (= len - window, at least 0) or j < sinks. They are walked in tiles
+// of 128 aligned positions: `first` tiles from position 0 (those of the sinks),
+// then the tiles from position `start` on, `tiles` in all. Of a tile only the
+// 32-position blocks from its first visible position to its last are read.
 struct SinkSpan {
-  int lo, n_sink, start, n;
-  __host__ __device__ __forceinline__ int position(int v) const { return v < n_sink ? v : start + (v - n_sink); }
+  int lo, first, start, tiles;
   __host__ __device__ __forceinline__ bool sees(int pos, int len, int sinks) const {
     return pos < len && (pos >= lo || pos < sinks);
   }
+  // first position and number of blocks to read of tile i
+  __host__ __device__ __forceinline__ int block0(int i, int len, int sinks, int* blocks) const {
+    const int p = i < first ? i * 128 : start + (i - first) * 128;
+    int from = p, to = p + 128 < len ? p + 128 : len;
+    if (lo > from && sinks <= from) from = lo & ~31;   // the window begins in it
+    if (lo >= p + 128 && sinks < to) to = sinks;       // the sinks end in it
+    *blocks = (to - from + 31) / 32;
+    return from;
+  }
 };
 
-__host__ __device__ __forceinline__ SinkSpan sink_span(int64_t len, int window, int sinks, int block) {
+__host__ __device__ __forceinline__ SinkSpan sink_span(int64_t len, int window, int sinks) {
   SinkSpan s;
   s.lo = len > window ? (int)(len - window) : 0;
-  s.n_sink = 0;
-  s.start = s.lo & ~(block - 1);
+  s.first = 0;
+  s.start = s.lo & ~127;
   if (sinks > 0) {
-    const int first = sinks < s.lo ? (sinks + block - 1) & ~(block - 1) : s.lo;  // end of the sinks' blocks
-    if (first < s.start)
-      s.n_sink = first;
+    const int end = sinks < s.lo ? sinks : s.lo;
+    if (((end + 127) & ~127) < s.start)
+      s.first = (end + 127) / 128;
     else
       s.start = 0;  // the runs meet
   }
-  s.n = s.n_sink + (int)(len - s.start);
+  s.tiles = s.first + (int)((len - s.start + 127) / 128);
   return s;
 }
 

@@ -12,12 +12,12 @@
 // splits: they are the CTAs of one cluster and merge through distributed
 // shared memory, without partial results in HBM or a second kernel.
 //
-// Visible keys are walked in a virtual order of whole 32-key blocks: those of
-// the sinks, then those from the one that holds the window's first key on (one
-// run when the two meet). A tile is the walked blocks of 128 aligned positions
-// (so it lies in one page; the first and last of a CTA's may have fewer than
-// four). The product is taken transposed, as in the multi-token kernel, so that
-// the keys fill the MMA's 128 rows and the few q heads are its columns:
+// Visible keys are walked in tiles of 128 aligned positions (each in one page):
+// those of the sinks, then those from the one that holds the window's first key
+// on (one run when the two meet); of a tile at an edge only the 32-key blocks
+// with visible keys are read. The product is taken transposed, as in the
+// multi-token kernel, so that the keys fill the MMA's 128 rows and the few q
+// heads are its columns:
 //   S^T = K Q^T    (M = 128 keys, N = 16, K = head_dim)
 //   O^T += V^T P^T (M = 128 value dims per MMA, N = 16, K = 32 keys per block)
 // A group has at most 8 heads and N is at least 16: columns 0..7 take the bf16
@@ -25,12 +25,12 @@
 // and the two halves are added, so neither rounding shows in the result.
 //
 // CTA = 224 threads: warp 0 loads 32 KB stages of 128 keys x 128 dims (one TMA
-// copy for a whole tile's stage, boxes of 32 keys for the others), warp 1
-// issues the MMAs (one lane) and owns TMEM, warps 2..5 rotate q and the new key,
-// run the softmax (thread = key = TMEM lane) and merge. Warp 6 puts the stages
-// of edge tiles in order before their MMAs: the new token's row, which is not
-// read back from the cache, and zeros in the rows of V that the query does not
-// see (they are masked in S and their weight is 0, but 0 * NaN is not).
+// copy, or boxes of 32 keys where a tile has fewer blocks), warp 1 issues the
+// MMAs and owns TMEM, warps 2..5 rotate q and the new key, run the softmax
+// (thread = key = TMEM lane) and merge. Warp 6 puts the stages of edge tiles in
+// order before their MMAs: the new token's row, which is not read back from the
+// cache, and zeros in the rows of V that the query does not see (they are
+// masked in S and their weight is 0, but 0 * NaN is not).
 //
 // HBM-bound: every visible K/V byte is read once per KV head (under K = V
 // the second read of a row hits L2).
@@ -52,7 +52,7 @@ namespace hlg {
 
 namespace {
 
-constexpr int BLK = 32;             // keys per block of the walk
+constexpr int BLK = 32;             // keys per block (SinkSpan)
 constexpr int BN = 128;             // keys per tile
 constexpr int NT = 224;             // threads
 constexpr int NQ = 16;              // MMA columns: 8 heads, then 8 remainders
@@ -186,57 +186,10 @@ __device__ __forceinline__ void turn4(const uint4& x, int c, int n_rot, const fl
   }
 }
 
-// The tiles of a CTA's blocks [blk0, blk0 + n_blk) of the walk: the walked
-// blocks of 128 aligned positions (one page), or all of them when there are at
-// most four (whatever their positions: a short split is one tile).
-struct Tile {
-  int i, nb, p0;  // first block, blocks, position of row 0
-};
-struct Walk {
-  SinkSpan sp;
-  int blk0, n_blk;
-  __device__ __forceinline__ int block_pos(int i) const { return sp.position((blk0 + i) * BLK); }
-  __device__ __forceinline__ Tile at(int i) const {
-    const int v = (blk0 + i) * BLK, p0 = sp.position(v);
-    int nb = n_blk - i;
-    if (n_blk > 4) {
-      nb = min(nb, 4 - ((p0 / BLK) & 3));
-      if (v < sp.n_sink) nb = min(nb, (sp.n_sink - v) / BLK);
-    }
-    return Tile{i, nb, p0};
-  }
-  // Blocks of t (bits) with rows that the query does not see among the first
-  // len_c positions of the sequence (the new token's row included).
-  __device__ __forceinline__ uint32_t edges(const Tile& t, int len_c, int sinks) const {
-    uint32_t e = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int p = block_pos(t.i + q);
-      if (q < t.nb && !(p + BLK <= len_c && (p >= sp.lo || p + BLK <= sinks))) e |= 1u << q;
-    }
-    return e;
-  }
-};
-
-// D[tmem] (+)= A[smem] * B[smem] with descriptors as (low word + offset, high word)
-__device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
-                                    uint32_t idesc, uint32_t accumulate) {
-  tc::mma_ss(d, (uint64_t)a_hi << 32 | a_lo, (uint64_t)b_hi << 32 | b_lo, idesc, accumulate);
-}
-
 struct Maps {
   CUtensorMap k, v;            // boxes of 128 keys x 128 dims
   CUtensorMap k_part, v_part;  // boxes of 32 keys x 64 dims
 };
-
-__device__ __forceinline__ void load_5d(uint32_t dst, const CUtensorMap* m, int row, int chunk, int head, int page,
-                                        uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(0), "r"(row), "r"(chunk), "r"(head), "r"(page)
-      : "memory");
-}
 
 template <int D, int CTAS>
 __global__ void __launch_bounds__(NT, CTAS)
@@ -266,13 +219,17 @@ __global__ void __launch_bounds__(NT, CTAS)
   }
   const bool has_new = a.k_new != nullptr;
   const int len_c = (int)len - (has_new ? 1 : 0);  // rows that are read from the cache
-  const SinkSpan sp = sink_span(len, a.window, a.sinks, BLK);
-  const int blocks = (sp.n + BLK - 1) / BLK;
-  const int per = (blocks + n_splits - 1) / n_splits;
-  const int blk0 = min(split * per, blocks);
-  const int n_blk = min(per, blocks - blk0);       // this CTA's blocks
-  const Walk walk{sp, blk0, n_blk};
-  const bool own_new = has_new && n_blk > 0 && blk0 + n_blk == blocks;  // its last block holds the new token
+  const SinkSpan sp = sink_span(len, a.window, a.sinks);
+  const int per = (sp.tiles + n_splits - 1) / n_splits;
+  const int tile0 = min(split * per, sp.tiles);
+  const int n_tiles = min(per, sp.tiles - tile0);
+  const bool own_new = has_new && n_tiles > 0 && tile0 + n_tiles == sp.tiles;  // the last tile holds the new token
+  // position of row 0 and 32-row blocks of this CTA's tile j
+  const auto tile = [&](int j, int* nb) { return sp.block0(tile0 + j, (int)len, a.sinks, nb); };
+  // whether tile j has rows that the query does not see among the cached ones
+  const auto is_edge = [&](int p0, int nb) {
+    return !(p0 + nb * BLK <= len_c && (p0 >= sp.lo || p0 + nb * BLK <= a.sinks));
+  };
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -309,176 +266,161 @@ __global__ void __launch_bounds__(NT, CTAS)
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
+    const uint32_t go = tc::elect_one();
+    if (go) {
       tc::prefetch_tmap(&maps.k);
       tc::prefetch_tmap(&maps.v);
       tc::prefetch_tmap(&maps.k_part);
       tc::prefetch_tmap(&maps.v_part);
-      const int32_t* table = a.page_table + (int64_t)b * a.pages_per_seq;
-      int item = 0;
-      bool ok = true;
-      const auto page_of = [&](int p0) {
-        int page = table[p0 / a.page_size];
-        if (page < 0 || page >= a.n_pages) {  // a page outside the pool: report it and read page 0 (finite, wrong)
-          set_status(a.status, GEMMA_ERR_DEVICE_RANGE);
-          page = 0;
-        }
-        return page;
-      };
-      const auto load = [&](const Tile& t, int page, bool isv) {
-        const CUtensorMap* whole = isv ? &maps.v : &maps.k;
-        const CUtensorMap* part = isv ? &maps.v_part : &maps.k_part;
-        const int row = t.p0 % a.page_size;
-        const bool one = t.nb == 4 && t.p0 % BN == 0 && walk.block_pos(t.i + 3) == t.p0 + 3 * BLK;
-        int prow[4] = {row, 0, 0, 0}, ppage[4] = {page, 0, 0, 0};
-        if (!one) {
-#pragma unroll
-          for (int q = 1; q < 4; ++q)
-            if (q < t.nb) {
-              const int p = walk.block_pos(t.i + q);
-              prow[q] = p % a.page_size;
-              ppage[q] = p / a.page_size == t.p0 / a.page_size ? page : page_of(p);
-            }
-        }
-        for (int h = 0; h < MT && ok; ++h, ++item) {
-          const int s = item % NS;
-          if (item >= NS)
-            ok = mbar_wait_bounded_at(&ctl->empty[s], ((item / NS) - 1) & 1, abort_flag, deadline, a.status, 51, item,
-                                      s, t.i);
-          if (!ok || *abort_flag) {
-            ok = false;
-            break;
-          }
-          if (a.drop_first_copy && item == 0 && split == 0 && g == 0 && b == 0) continue;
-          const uint32_t dst = base + s * STAGE_B, bar = smem_u32(&ctl->full[s]);
-          mbar_arrive_expect_tx(&ctl->full[s], (uint32_t)(t.nb * 2 * BOX_B));
-          ctl->issued = item + 1;
-          if (one) {
-            load_5d(dst, whole, row, h * 2, g, page, bar);
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (q < t.nb) {
-                load_5d(dst + q * BOX_B, part, prow[q], h * 2, g, ppage[q], bar);
-                load_5d(dst + CH_B + q * BOX_B, part, prow[q], h * 2 + 1, g, ppage[q], bar);
-              }
-          }
-        }
-      };
-      // K_0, K_1, V_0, K_2, V_1, ...; the next tile's table entry is read a tile ahead
-      Tile t = walk.at(0), pt = t;
-      int page = n_blk > 0 ? page_of(t.p0) : 0, ppage = 0;
-      for (int i = 0; i < n_blk && ok;) {
-        const int next = i + t.nb;
-        const Tile nt = walk.at(min(next, n_blk - 1));
-        const int npage = next < n_blk ? page_of(nt.p0) : 0;
-        load(t, page, false);
-        if (i > 0 && ok) load(pt, ppage, true);
-        pt = t;
-        ppage = page;
-        t = nt;
-        page = npage;
-        i = next;
-      }
-      if (n_blk > 0 && ok) load(pt, ppage, true);
     }
+    const int32_t* table = a.page_table + (int64_t)b * a.pages_per_seq;
+    int item = 0;
+    bool ok = true;
+    const auto load = [&](int p0, int nb, int entry, bool isv) {
+      const bool outside = entry < 0 || entry >= a.n_pages;  // report it and read page 0 (finite, wrong)
+      if (outside && go) set_status(a.status, GEMMA_ERR_DEVICE_RANGE);
+      const int page = outside ? 0 : entry, row = p0 % a.page_size;
+      // one copy may read rows past the tile's blocks, which nothing uses (past
+      // the page they arrive as zeros): worth it for one block in four, or
+      // where the call leaves HBM idle
+      const bool one = CTAS == 1 || nb >= 3;
+      const CUtensorMap* map = one ? (isv ? &maps.v : &maps.k) : (isv ? &maps.v_part : &maps.k_part);
+      const uint32_t bytes = one ? STAGE_B : nb * 2 * BOX_B;
+      for (int h = 0; h < MT; ++h, ++item) {
+        const int s = item % NS;
+        if (item >= NS)
+          ok = wait_all(&ctl->empty[s], ((item / NS) - 1) & 1, abort_flag, deadline, a.status, 51, item, s, p0);
+        ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+        if (!ok) break;
+        if (a.drop_first_copy && item == 0 && split == 0 && g == 0 && b == 0) continue;
+        const uint32_t dst = base + s * STAGE_B, bar = smem_u32(&ctl->full[s]);
+        if (go) {
+          mbar_arrive_expect_tx(&ctl->full[s], bytes);
+          ctl->issued = item + 1;
+        }
+        __syncwarp();
+        tc::tma_load_5d_if(go, dst, map, 0, row, h * 2, g, page, bar);
+        if (!one) {
+          tc::tma_load_5d_if(go, dst + CH_B, map, 0, row, h * 2 + 1, g, page, bar);
+          if (nb > 1) {
+            tc::tma_load_5d_if(go, dst + BOX_B, map, 0, row + BLK, h * 2, g, page, bar);
+            tc::tma_load_5d_if(go, dst + CH_B + BOX_B, map, 0, row + BLK, h * 2 + 1, g, page, bar);
+          }
+        }
+      }
+    };
+    // K_0, K_1, V_0, K_2, V_1, ...; a tile's table entry is read a tile ahead
+    int nb = 0, pnb = 0, p0 = 0, pp0 = 0, entry = 0, pentry = 0;
+    if (n_tiles > 0) {
+      p0 = tile(0, &nb);
+      entry = table[p0 / a.page_size];
+    }
+    for (int j = 0; j < n_tiles && ok; ++j) {
+      int nnb = 0, np0 = 0, nentry = 0;
+      if (j + 1 < n_tiles) {
+        np0 = tile(j + 1, &nnb);
+        nentry = table[np0 / a.page_size];
+      }
+      load(p0, nb, entry, false);
+      if (j > 0 && ok) load(pp0, pnb, pentry, true);
+      pp0 = p0, pnb = nb, pentry = entry;
+      p0 = np0, nb = nnb, entry = nentry;
+    }
+    if (n_tiles > 0 && ok) load(pp0, pnb, pentry, true);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      bool ok = n_blk == 0 ||
-                mbar_wait_bounded_at(&ctl->q_ready, 0, abort_flag, deadline, a.status, 50, 0, 0, 0);
-      const uint64_t dk = tc::smem_desc_sw128(base, 16, 1024), dv = tc::smem_desc_sw128(base, CH_B, 1024);
-      const uint64_t dq = tc::smem_desc_sw128(base + C::Q_OFF, 16, 1024);
-      const uint32_t k_hi = (uint32_t)(dk >> 32), v_hi = (uint32_t)(dv >> 32), q_hi = (uint32_t)(dq >> 32);
-      const uint32_t q_lo = (uint32_t)dq, p_lo = q_lo + ((C::P_OFF - C::Q_OFF) >> 4);
-      int item = 0, taken = 0;
-      uint32_t patches = 0;  // parity of each slot's next patch
-      // waits for the next stage (and its patch); returns its slot
-      const auto take = [&](bool patch) {
-        const int s = item % NS;
-        uint64_t* bar = patch ? &ctl->patched[s] : &ctl->full[s];
-        const uint32_t parity = patch ? patches >> s & 1u : (uint32_t)(item / NS) & 1u;
-        ok = mbar_wait_bounded_at(bar, parity, abort_flag, deadline, a.status, 52, item, s, patch);
-        if (patch) patches ^= 1u << s;
-        tc::fence_after_sync();
-        ++item;
-        if (ok) taken = item;
-        return s;
-      };
-      const auto values = [&](const Tile& t, int j) {  // O^T += V_j^T P_j^T
-        const bool patch = walk.edges(t, len_c, a.sinks) != 0;
-        if (patch) mbar_arrive(&ctl->patch_req);
-        ok = mbar_wait_bounded_at(&ctl->p_ready[j & 1], (j >> 1) & 1, abort_flag, deadline, a.status, 53, j, 0, 0);
-        const uint32_t pj = p_lo + (j & 1) * (P_B >> 4);
-        for (int m = 0; m < MT && ok; ++m) {
-          const int s = take(patch);
-          if (!ok) break;
-          // V^T: 128 dims (two 64-dim boxes CH_B apart) x 16 keys; P^T: 16 columns x 16 keys
-          const uint32_t v_lo = (uint32_t)dv + s * (STAGE_B >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            if (kk < 2 * t.nb)
-              mma(tmem + m * NQ, v_lo + kk * (2048 >> 4), v_hi, pj + (kk >> 2) * (NQ * 128 >> 4) + (kk & 3) * 2, q_hi,
-                  IDESC_OT, (j > 0 || kk) ? 1u : 0u);
-          tc::commit(smem_u32(&ctl->empty[s]));
-        }
-        if (ok) tc::commit(smem_u32(&ctl->o_done[j & 1]));
-      };
-      Tile t = walk.at(0), pt = t;
-      int j = 0;
-      for (int i = 0; i < n_blk && ok; i += t.nb, ++j) {
-        t = walk.at(i);
-        const bool patch = own_new && i + t.nb == n_blk;
-        if (patch) mbar_arrive(&ctl->patch_req);
-        for (int h = 0; h < MT; ++h) {  // S_j^T = K_j Q^T
-          const int s = take(patch);
-          if (!ok) break;
-          const uint32_t k_lo = (uint32_t)dk + s * (STAGE_B >> 4), qh = q_lo + h * (2 * NQ * 128 >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma(tmem + C::COL_S + (j & 1) * NQ, k_lo + (kk >> 2) * (CH_B >> 4) + (kk & 3) * 2, k_hi,
-                qh + (kk >> 2) * (NQ * 128 >> 4) + (kk & 3) * 2, q_hi, IDESC_ST, (h | kk) != 0);
-          tc::commit(smem_u32(&ctl->empty[s]));
-        }
+    const uint32_t go = tc::elect_one();
+    bool ok = n_tiles == 0 || wait_all(&ctl->q_ready, 0, abort_flag, deadline, a.status, 50, 0, 0, 0);
+    const uint64_t dk = tc::smem_desc_sw128(base, 16, 1024), dv = tc::smem_desc_sw128(base, CH_B, 1024);
+    const uint64_t dq = tc::smem_desc_sw128(base + C::Q_OFF, 16, 1024), dp = dq + ((C::P_OFF - C::Q_OFF) >> 4);
+    int item = 0, taken = 0;
+    uint32_t patches = 0;  // parity of each slot's next patch
+    // waits for the next stage (and its patch); returns its slot
+    const auto take = [&](bool patch) {
+      const int s = item % NS;
+      const uint32_t parity = patch ? patches >> s & 1u : (uint32_t)(item / NS) & 1u;
+      ok = wait_all(patch ? &ctl->patched[s] : &ctl->full[s], parity, abort_flag, deadline, a.status, 52, item, s,
+                    patch);
+      if (patch) patches ^= 1u << s;
+      tc::fence_after_sync();
+      ++item;
+      if (ok) taken = item;
+      return s;
+    };
+    const auto values = [&](int p0, int nb, int j) {  // O^T += V_j^T P_j^T
+      const bool patch = is_edge(p0, nb);
+      if (patch && go) mbar_arrive(&ctl->patch_req);
+      ok = wait_all(&ctl->p_ready[j & 1], (j >> 1) & 1, abort_flag, deadline, a.status, 53, j, 0, 0);
+      const uint64_t pj = dp + (uint64_t)((j & 1) * (P_B >> 4));
+      for (int m = 0; m < MT && ok; ++m) {
+        const int s = take(patch);
         if (!ok) break;
-        tc::commit(smem_u32(&ctl->s_full[j & 1]));
-        if (j > 0) values(pt, j - 1);
-        pt = t;
+        // V^T: 128 dims (two 64-dim boxes CH_B apart) x 16 keys; P^T: 16 columns x 16 keys
+        const uint64_t v = dv + (uint64_t)(s * (STAGE_B >> 4));
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          if (kk < 2 * nb)
+            tc::mma_ss_if(go, tmem + m * NQ, v + kk * (2048 >> 4),
+                          pj + (kk >> 2) * (NQ * 128 >> 4) + (kk & 3) * 2, IDESC_OT, (j > 0 || kk) ? 1u : 0u);
+        tc::commit_if(go, smem_u32(&ctl->empty[s]));
       }
-      if (n_blk > 0 && ok) values(pt, j - 1);
-      ctl->taken = taken;
-      // no MMA may be in flight when TMEM or shared memory is released
-      tc::commit(smem_u32(&ctl->drain));
-      volatile int never = 0;
-      mbar_wait_bounded_at(&ctl->drain, 0, &never, globaltimer_ns() + 200000000ull, a.status, 55, 0, 0, 0);
+      if (ok) tc::commit_if(go, smem_u32(&ctl->o_done[j & 1]));
+    };
+    int pp0 = 0, pnb = 0;
+    for (int j = 0; j < n_tiles && ok; ++j) {
+      int nb;
+      const int p0 = tile(j, &nb);
+      const bool patch = own_new && j == n_tiles - 1;
+      if (patch && go) mbar_arrive(&ctl->patch_req);
+      for (int h = 0; h < MT; ++h) {  // S_j^T = K_j Q^T
+        const int s = take(patch);
+        if (!ok) break;
+        const uint64_t k = dk + (uint64_t)(s * (STAGE_B >> 4)), qh = dq + (uint64_t)(h * (2 * NQ * 128 >> 4));
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_ss_if(go, tmem + C::COL_S + (j & 1) * NQ, k + (kk >> 2) * (CH_B >> 4) + (kk & 3) * 2,
+                        qh + (kk >> 2) * (NQ * 128 >> 4) + (kk & 3) * 2, IDESC_ST, (h | kk) != 0);
+        tc::commit_if(go, smem_u32(&ctl->empty[s]));
+      }
+      if (!ok) break;
+      tc::commit_if(go, smem_u32(&ctl->s_full[j & 1]));
+      if (j > 0) values(pp0, pnb, j - 1);
+      pp0 = p0;
+      pnb = nb;
     }
+    if (n_tiles > 0 && ok) values(pp0, pnb, n_tiles - 1);
+    // no MMA may be in flight when TMEM or shared memory is released
+    tc::commit_if(go, smem_u32(&ctl->drain));
+    volatile int never = 0;
+    mbar_wait_bounded_at(&ctl->drain, 0, &never, globaltimer_ns() + 200000000ull, a.status, 55, 0, 0, 0);
+    if (go) ctl->taken = taken;
   } else if (warp == 6) {
     // ------------------------------------------------------------ edge rows
     // Same order of stages as the issuer's, which asks for each group of MT
     // that needs this warp once it has waited for all stages before it: the
     // parity waits here cannot mistake an older phase for the stage's own.
     // lane: 16-byte unit lane % 16 (of the 128 dims) of every second row.
-    bool ok = n_blk == 0 || wait_all(&ctl->q_ready, 0, abort_flag, deadline, a.status, 61, 0, 0, 0);
+    bool ok = n_tiles == 0 || wait_all(&ctl->q_ready, 0, abort_flag, deadline, a.status, 61, 0, 0, 0);
     const int cc = (lane >> 3) & 1, u = lane & 7;
     int item = 0, groups = 0;
-    // rows of t to clear (V), then the new token's row
-    const auto patch = [&](const Tile& t, bool isv) {
-      const uint32_t edge = isv ? walk.edges(t, len_c, a.sinks) : 0u;
-      const bool with_new = own_new && t.i + t.nb == n_blk;
-      if (!edge && !with_new) {
+    // rows of tile j to clear (V), then the new token's row
+    const auto patch = [&](int j, bool isv) {
+      int nb;
+      const int p0 = tile(j, &nb);
+      const bool with_new = own_new && j == n_tiles - 1;
+      if (!(isv && is_edge(p0, nb)) && !with_new) {
         item += MT;
         return;
       }
-      ok = wait_all(&ctl->patch_req, groups++ & 1, abort_flag, deadline, a.status, 63, t.i, 0, 0);
+      ok = wait_all(&ctl->patch_req, groups++ & 1, abort_flag, deadline, a.status, 63, j, 0, 0);
       uint32_t off[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        off[q] = ~__ballot_sync(0xffffffffu, !(edge >> q & 1) ||
-                                                 sp.sees(walk.block_pos(t.i + q) + lane, len_c, a.sinks));
-      const int new_row = (t.nb - 1) * BLK + len_c - walk.block_pos(t.i + t.nb - 1);
+        off[q] = __ballot_sync(0xffffffffu, isv && q < nb && !sp.sees(p0 + q * BLK + lane, len_c, a.sinks));
+      const int new_row = len_c - p0;
       for (int h = 0; h < MT && ok; ++h, ++item) {
         const int s = item % NS;
-        ok = wait_all(&ctl->full[s], (item / NS) & 1, abort_flag, deadline, a.status, 62, item, s, t.i);
+        ok = wait_all(&ctl->full[s], (item / NS) & 1, abort_flag, deadline, a.status, 62, item, s, j);
         if (!ok) break;
         unsigned char* st = sm + s * STAGE_B + cc * CH_B;
 #pragma unroll
@@ -502,21 +444,18 @@ __global__ void __launch_bounds__(NT, CTAS)
         if (lane == 0) mbar_arrive(&ctl->patched[s]);
       }
     };
-    Tile t = walk.at(0), pt = t;
-    for (int i = 0; i < n_blk && ok; i += t.nb) {
-      t = walk.at(i);
-      patch(t, false);
-      if (i > 0 && ok) patch(pt, true);
-      pt = t;
+    for (int j = 0; j < n_tiles && ok; ++j) {
+      patch(j, false);
+      if (j > 0 && ok) patch(j - 1, true);
     }
-    if (n_blk > 0 && ok) patch(pt, true);
+    if (n_tiles > 0 && ok) patch(n_tiles - 1, true);
   } else {
     // ------------------------------------------------------------ rotation, softmax
     const int q4 = warp & 3;
     const int kl = q4 * 32 + lane;  // this thread's key of a tile = its TMEM lane
     const int t128 = tid - 64;
     const uint32_t tm = tmem + ((uint32_t)(q4 * 32) << 16);
-    if (n_blk > 0) {
+    if (n_tiles > 0) {
       // Q^T rows 0..7: heads, 8..15: their remainders; 128-byte rows of 64
       // dims, 16-byte units swizzled by the row
       uint4 x[8 * CH / 128];
@@ -572,10 +511,9 @@ __global__ void __launch_bounds__(NT, CTAS)
     // for all of them.
     bool bad = false;
     int pv_seen = 0;  // PV_0 .. PV_{pv_seen-1} are known complete
-    int j = 0;
-    Tile t{0, 0, 0};
-    for (int i = 0; i < n_blk; i += t.nb, ++j) {
-      t = walk.at(i);
+    for (int j = 0; j < n_tiles; ++j) {
+      int nb;
+      const int p0 = tile(j, &nb);
       if (!bad && !wait_all(&ctl->s_full[j & 1], (j >> 1) & 1, abort_flag, deadline, a.status, 56, j, 0, 0)) bad = true;
       tc::fence_after_sync();
       float v[8];
@@ -583,7 +521,7 @@ __global__ void __launch_bounds__(NT, CTAS)
         uint32_t r[16];
         tmem_ld16(tm + C::COL_S + (uint32_t)(j & 1) * NQ, r);
         tc::tmem_wait_ld();
-        const bool seen = kl < t.nb * BLK && sp.sees(walk.block_pos(t.i + (kl >> 5)) + (kl & 31), (int)len, a.sinks);
+        const bool seen = kl < nb * BLK && sp.sees(p0 + kl, (int)len, a.sinks);
 #pragma unroll
         for (int n = 0; n < 8; ++n)
           v[n] = seen ? (__uint_as_float(r[n]) + __uint_as_float(r[n + 8])) * a.scale_log2 : -INFINITY;
@@ -657,8 +595,9 @@ __global__ void __launch_bounds__(NT, CTAS)
       tc::fence_before_sync();
       mbar_arrive(&ctl->p_ready[j & 1]);
     }
-    if (!bad && n_blk > 0)
-      bad = !wait_all(&ctl->o_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, deadline, a.status, 59, j, 0, 0);
+    if (!bad && n_tiles > 0)
+      bad = !wait_all(&ctl->o_done[(n_tiles - 1) & 1], ((n_tiles - 1) >> 1) & 1, abort_flag, deadline, a.status, 59,
+                      n_tiles, 0, 0);
     good = !any128(bad);
     // sums over the tile's 128 key lanes
     const float s = reduce8<false>(l, lane);
@@ -687,7 +626,7 @@ __global__ void __launch_bounds__(NT, CTAS)
     if (kl < n_splits * 8)
       st_cluster2(pair::map_to(smem_u32(&ctl->ml[split][kl & 7]), kl >> 3), ctl->m[kl & 7],
                   good ? ctl->l[kl & 7] : -1.f);
-    if (n_blk > 0) {
+    if (n_tiles > 0) {
       tc::fence_after_sync();
       const uint32_t tm = tmem + ((uint32_t)((warp & 3) * 32) << 16);
       uint32_t o[MT][16];
@@ -772,15 +711,14 @@ cudaError_t launch_as(const Maps& maps, const SinkDecodeArgs& a, int B, int n_sp
 }
 
 // Splits per (sequence, KV head): the power of two up to MAX_CLUSTER that
-// minimises (waves of CTAs) x (keys per CTA + a fixed cost per CTA, in keys).
+// minimises (waves of CTAs) x (tiles per CTA + a fixed cost per CTA of one tile).
 int plan_splits(int B, int Hkv, int window, int sinks, int max_len) {
-  const SinkSpan sp = sink_span(max_len, window, sinks, BLK);
+  const SinkSpan sp = sink_span(max_len, window, sinks);
   const int64_t pairs = (int64_t)B * Hkv, wave = (int64_t)multiprocessors() * 2;
   int best = 1;
   int64_t best_cost = INT64_MAX;
   for (int n = 1; n <= MAX_CLUSTER; n *= 2) {
-    const int64_t keys = (sp.n + n - 1) / n;
-    const int64_t cost = ((pairs * n + wave - 1) / wave) * (keys + 128);
+    const int64_t cost = ((pairs * n + wave - 1) / wave) * ((sp.tiles + n - 1) / n + 1);
     if (cost < best_cost) {
       best_cost = cost;
       best = n;

@@ -198,36 +198,45 @@ def test_struct_fields_match_the_header(name):
 
 
 # ------------------------------------------------------------ the decode kernel's walk
-def span(length, window, sinks, block):
-    """sink_span of csrc/common.cuh, restated: (lo, n_sink, start, n)."""
+def walk(length, window, sinks):
+    """sink_span and block0 of csrc/common.cuh, restated: [(first position, 32-position blocks)] of every tile."""
     lo = max(0, length - window)
-    n_sink, start = 0, lo // block * block
+    first, start = 0, lo // 128 * 128
     if sinks > 0:
-        first = -(-sinks // block) * block if sinks < lo else lo
-        if first < start:
-            n_sink = first
+        end = min(sinks, lo)
+        if -(-end // 128) * 128 < start:
+            first = -(-end // 128)
         else:
             start = 0
-    return lo, n_sink, start, n_sink + length - start
+    out = []
+    for i in range(first + -(-(length - start) // 128)):
+        p = i * 128 if i < first else start + (i - first) * 128
+        begin, to = p, min(p + 128, length)
+        if lo > begin and sinks <= begin:
+            begin = lo // 32 * 32
+        if lo >= p + 128 and sinks < to:
+            to = sinks
+        out.append((begin, -(-(to - begin) // 32)))
+    return out
 
 
-@pytest.mark.parametrize("block", [32, 64])
-@pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 64, 100, 1 << 30])
-@pytest.mark.parametrize("sinks", [0, 1, 31, 32, 33, 70, 300, 1 << 30])
-def test_walk_covers_every_visible_key_once(window, sinks, block):
-    for length in [1, 2, 31, 32, 33, 64, 65, 100, 131, 200, 333, 400]:
-        lo, n_sink, start, n = span(length, window, sinks, block)
-        assert start % block == 0 and n_sink % block == 0 and 0 < n <= length
-        walked = [v if v < n_sink else start + v - n_sink for v in range(n)]
-        assert len(set(walked)) == n and max(walked) == length - 1
-        seen = [p for p in walked if p >= lo or p < sinks]
+@pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 64, 100, 128, 129, 300, 1 << 30])
+@pytest.mark.parametrize("sinks", [0, 1, 31, 32, 33, 70, 128, 129, 300, 1 << 30])
+def test_walk_covers_every_visible_key_once(window, sinks):
+    for length in [1, 2, 31, 32, 33, 64, 65, 127, 128, 129, 200, 256, 333, 400, 513, 700]:
+        lo = max(0, length - window)
+        tiles = walk(length, window, sinks)
+        read = []
+        for begin, blocks in tiles:
+            rows = list(range(begin, begin + 32 * blocks))
+            # in one aligned 128-position tile, whole blocks, the first and the last with a visible key
+            assert begin % 32 == 0 and 1 <= blocks <= 4 and begin // 128 == rows[-1] // 128
+            for block in (rows[:32], rows[-32:]):
+                assert any(p < length and (p >= lo or p < sinks) for p in block), (length, begin, blocks)
+            read += rows
+        assert len(set(read)) == len(read) and length - 1 in range(tiles[-1][0], tiles[-1][0] + 32 * tiles[-1][1])
+        seen = [p for p in read if p < length and (p >= lo or p < sinks)]
         assert seen == [j for j in range(length) if sees(j, length - 1, window, sinks)]
-        # every block of the walk is a whole block of positions; two runs only where each block has a visible key
-        for v in range(0, n, block):
-            tile = walked[v:v + block]
-            assert tile[0] % block == 0 and tile == list(range(tile[0], tile[0] + len(tile)))
-            if n_sink:
-                assert any(p >= lo or p < sinks for p in tile)
 
 
 def test_reference_book_and_attention_are_what_they_say():

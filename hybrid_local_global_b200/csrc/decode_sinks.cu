@@ -41,6 +41,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -60,7 +61,7 @@ constexpr int CH_B = BN * 128;      // [128 keys][64 dims], swizzled
 constexpr int STAGE_B = 2 * CH_B;   // 128 dims of a K or V tile
 constexpr int BOX_B = BLK * 128;    // one TMA box: 32 keys x 64 dims
 constexpr int P_B = 2 * NQ * 128;   // P^T: two chunks of 64 keys
-constexpr int MAX_CLUSTER = 8;      // CTAs per (sequence, KV head)
+constexpr int MAX_CLUSTER = 16;     // CTAs per (sequence, KV head); above 8 where the device allows it
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr double kInvPi = 0.31830988618379067153776752674503;
 constexpr uint32_t IDESC_ST = tc::idesc_bf16_f32(128, NQ, 0, 0);  // K (K-major) x Q (K-major)
@@ -691,40 +692,89 @@ __global__ void __launch_bounds__(NT, CTAS)
 }
 
 template <int D, int CTAS>
-cudaError_t launch_as(const Maps& maps, const SinkDecodeArgs& a, int B, int n_splits, cudaStream_t st) {
-  using C = Cfg<D, CTAS>;
-  cudaError_t e = cudaFuncSetAttribute(k_decode_sinks<D, CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(n_splits, a.Hkv, B);
-  cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = n_splits;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_decode_sinks<D, CTAS>, maps, a);
+void config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* at, int n_splits, int Hkv, int B, cudaStream_t st) {
+  *cfg = cudaLaunchConfig_t{};
+  cfg->gridDim = dim3(n_splits, Hkv, B);
+  cfg->blockDim = dim3(NT);
+  cfg->dynamicSmemBytes = Cfg<D, CTAS>::SMEM;
+  cfg->stream = st;
+  at->id = cudaLaunchAttributeClusterDimension;
+  at->val.clusterDim.x = n_splits;
+  at->val.clusterDim.y = 1;
+  at->val.clusterDim.z = 1;
+  cfg->attrs = at;
+  cfg->numAttrs = 1;
 }
 
-// Splits per (sequence, KV head): the power of two up to MAX_CLUSTER that
-// minimises (waves of CTAs) x (tiles per CTA + a fixed cost per CTA of one tile).
-int plan_splits(int B, int Hkv, int window, int sinks, int max_len) {
-  const SinkSpan sp = sink_span(max_len, window, sinks);
-  const int64_t pairs = (int64_t)B * Hkv, wave = (int64_t)multiprocessors() * 2;
-  int best = 1;
-  int64_t best_cost = INT64_MAX;
-  for (int n = 1; n <= MAX_CLUSTER; n *= 2) {
-    const int64_t cost = ((pairs * n + wave - 1) / wave) * ((sp.tiles + n - 1) / n + 1);
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = n;
+// Clusters of 2^log_n CTAs that the device holds at once with one CTA per SM
+// (0: none): a property of the device, asked once. Sets the attributes of
+// both instances.
+template <int D>
+int resident(int log_n) {
+  static std::mutex mu;
+  static int known[128][5];  // 1 + the answer
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 0;
+  std::lock_guard<std::mutex> lk(mu);
+  int& k = known[dev][log_n];
+  if (!k) {
+    const auto one = k_decode_sinks<D, 1>;
+    const auto two = k_decode_sinks<D, 2>;
+    const auto smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    const auto large = cudaFuncAttributeNonPortableClusterSizeAllowed;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute at;
+    config<D, 1>(&cfg, &at, 1 << log_n, 1, 1, nullptr);
+    int n = 0;
+    if (cudaFuncSetAttribute(one, smem, Cfg<D, 1>::SMEM) != cudaSuccess ||
+        cudaFuncSetAttribute(two, smem, Cfg<D, 2>::SMEM) != cudaSuccess ||
+        (log_n > 3 && (cudaFuncSetAttribute(one, large, 1) != cudaSuccess ||
+                       cudaFuncSetAttribute(two, large, 1) != cudaSuccess)) ||
+        cudaOccupancyMaxActiveClusters(&n, one, &cfg) != cudaSuccess) {
+      n = 0;
+      (void)cudaGetLastError();  // this size is not to be had: another one is taken
     }
+    k = 1 + n;
   }
-  return best;
+  return k - 1;
+}
+
+template <int D>
+cudaError_t launch(const Maps& maps, const SinkDecodeArgs& a, int B, cudaStream_t st) {
+  // The split (a power of two, up to one cluster) and one or two CTAs per SM
+  // that look quickest. A tile of 2 x 128 keys takes a CTA that has its SM to
+  // itself 2.8 us at head_dim 512 and one that shares it 5.5 us; a wave of
+  // clusters costs 8 us besides, and HBM gives 6500 bytes a ns. Measured with
+  // every choice: 4096 keys, 4 KV heads, 4 sequences: 32 us (4 CTAs each, alone),
+  // 36 (8, shared), 48 (8, alone: the clusters do not fit at once), 96 (1, alone);
+  // 64 sequences: 314 us (1, shared), 316 (2), 333 (4), 367 (8).
+  const SinkSpan sp = sink_span(a.max_len, a.window, a.sinks);
+  const double tile = D / 512.0, pairs = (double)B * a.Hkv;
+  const double hbm = pairs * sp.tiles * (a.keqv ? 1 : 2) * (BN * D * 2.0) / 6.5e6;
+  double best = 1e300;
+  int best_n = 0, best_ctas = 2;
+  for (int log_n = 0; log_n < 5; ++log_n)
+    for (int ctas = 1; ctas <= 2; ++ctas) {
+      const int fit = ctas * resident<D>(log_n);
+      if (fit <= 0) continue;
+      const int per = (sp.tiles + (1 << log_n) - 1) >> log_n;
+      const double waves = std::ceil(pairs / fit);
+      const double cost = std::max(waves * per * tile * (ctas == 1 ? 2.8 : 5.5), hbm) + 8.0 * waves;
+      if (cost < best) {
+        best = cost;
+        best_n = 1 << log_n;
+        best_ctas = ctas;
+      }
+    }
+  if (!best_n) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute at;
+  if (best_ctas == 1) {
+    config<D, 1>(&cfg, &at, best_n, a.Hkv, B, st);
+    return cudaLaunchKernelEx(&cfg, k_decode_sinks<D, 1>, maps, a);
+  }
+  config<D, 2>(&cfg, &at, best_n, a.Hkv, B, st);
+  return cudaLaunchKernelEx(&cfg, k_decode_sinks<D, 2>, maps, a);
 }
 
 }  // namespace
@@ -746,10 +796,7 @@ cudaError_t launch_decode_sinks(SinkDecodeArgs& a, int B, int D, double log2_the
              !make_map_bf16_5d(&maps.v_part, a.v_pool, dims, str, part)) {
     return cudaErrorInvalidValue;
   }
-  const int n = plan_splits(B, a.Hkv, a.window, a.sinks, a.max_len);
-  const bool deep = (int64_t)B * a.Hkv * n <= multiprocessors();
-  if (D == 256) return deep ? launch_as<256, 1>(maps, a, B, n, st) : launch_as<256, 2>(maps, a, B, n, st);
-  return deep ? launch_as<512, 1>(maps, a, B, n, st) : launch_as<512, 2>(maps, a, B, n, st);
+  return D == 256 ? launch<256>(maps, a, B, st) : launch<512>(maps, a, B, st);
 }
 
 }  // namespace hlg

@@ -22,7 +22,8 @@
 //   O^T += V^T P^T (M = 128 value dims per MMA, N = 16, K = 32 keys per block)
 // A group has at most 8 heads and N is at least 16: columns 0..7 take the bf16
 // values of Q~ (and of the weights P), columns 8..15 what that rounding lost,
-// and the two halves are added, so neither rounding shows in the result.
+// and the two halves are added, so neither rounding shows in the result. The new
+// token's logits are 32-bit sums.
 //
 // CTA = 224 threads: warp 0 loads 32 KB stages of 128 keys x 128 dims (one TMA
 // copy, or boxes of 32 keys where a tile has fewer blocks), warp 1 issues the
@@ -79,6 +80,7 @@ struct Ctl {
   int abort;
   int issued, taken;              // stages loaded, stages whose load was waited for
   float m[8], f[8], l[8];         // running maxima, rescale factors, sums (this CTA)
+  float s_new[4][8];              // the new key's logits, partial sums of each softmax warp
   float red[4][8];
   alignas(16) float wgt[MAX_CLUSTER][8];
   float2 ml[MAX_CLUSTER][8];      // the cluster's (m, l); l < 0: that CTA gave up
@@ -90,16 +92,16 @@ template <int D, int CTAS>
 struct Cfg {
   static constexpr int MT = D / 128;                 // K stages per tile = O^T blocks = V stages per tile
   static constexpr int Q_B = (D / 64) * NQ * 128;
-  static constexpr int NS = CTAS == 2 ? 2 : 6;
+  static constexpr int NS = CTAS == 2 ? 2 : D == 512 ? 5 : 6;
   static constexpr int Q_OFF = NS * STAGE_B;
   static constexpr int P_OFF = Q_OFF + Q_B;          // two buffers; the angles before the first tile
   static constexpr int NEW_OFF = P_OFF + 2 * P_B;    // the new token's K row, V row
-  static constexpr int CTL_OFF = NEW_OFF + 2 * D * 2;
+  static constexpr int MERGE_OFF = NEW_OFF + 2 * D * 2;  // [split][column][head]: this CTA's columns of every O^T
+  static constexpr int CTL_OFF = MERGE_OFF + 8 * D * 4;
   static constexpr int SMEM = 1024 + CTL_OFF + (int)sizeof(Ctl<NS>);
   static constexpr uint32_t COL_S = MT * NQ;         // after O^T
   static constexpr uint32_t TMEM_COLS = MT * NQ + 2 * NQ <= 64 ? 64 : 128;
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "resident CTAs");
-  static_assert(8 * D * 4 <= NS * STAGE_B, "the merge buffer overlays the drained ring");
   static_assert((D / 2) * 8 <= 2 * P_B, "angles");
 };
 
@@ -255,8 +257,16 @@ __global__ void __launch_bounds__(NT, CTAS)
     tc::tmem_relinquish();
   }
   tc::fence_before_sync();
+  // (producer) the first tile's table entry, ahead of the barriers
+  const int32_t* table = a.page_table + (int64_t)b * a.pages_per_seq;
+  int nb0 = 0, p0_0 = 0, entry0 = 0;
+  if (warp == 0 && n_tiles > 0) {
+    p0_0 = tile(0, &nb0);
+    entry0 = table[p0_0 / a.page_size];
+  }
   __syncwarp();
   __syncthreads();
+  pair::cluster_arrive();  // this CTA runs: its shared memory may be written by the others
   tc::fence_after_sync();
   const uint32_t tmem = ctl->tmem_base;
   const uint64_t deadline = globaltimer_ns() + a.wait_ns;
@@ -274,7 +284,6 @@ __global__ void __launch_bounds__(NT, CTAS)
       tc::prefetch_tmap(&maps.k_part);
       tc::prefetch_tmap(&maps.v_part);
     }
-    const int32_t* table = a.page_table + (int64_t)b * a.pages_per_seq;
     int item = 0;
     bool ok = true;
     const auto load = [&](int p0, int nb, int entry, bool isv) {
@@ -311,11 +320,7 @@ __global__ void __launch_bounds__(NT, CTAS)
       }
     };
     // K_0, K_1, V_0, K_2, V_1, ...; a tile's table entry is read a tile ahead
-    int nb = 0, pnb = 0, p0 = 0, pp0 = 0, entry = 0, pentry = 0;
-    if (n_tiles > 0) {
-      p0 = tile(0, &nb);
-      entry = table[p0 / a.page_size];
-    }
+    int nb = nb0, pnb = 0, p0 = p0_0, pp0 = 0, entry = entry0, pentry = 0;
     for (int j = 0; j < n_tiles && ok; ++j) {
       int nnb = 0, np0 = 0, nentry = 0;
       if (j + 1 < n_tiles) {
@@ -371,10 +376,8 @@ __global__ void __launch_bounds__(NT, CTAS)
     for (int j = 0; j < n_tiles && ok; ++j) {
       int nb;
       const int p0 = tile(j, &nb);
-      const bool patch = own_new && j == n_tiles - 1;
-      if (patch && go) mbar_arrive(&ctl->patch_req);
       for (int h = 0; h < MT; ++h) {  // S_j^T = K_j Q^T
-        const int s = take(patch);
+        const int s = take(false);
         if (!ok) break;
         const uint64_t k = dk + (uint64_t)(s * (STAGE_B >> 4)), qh = dq + (uint64_t)(h * (2 * NQ * 128 >> 4));
 #pragma unroll
@@ -397,28 +400,25 @@ __global__ void __launch_bounds__(NT, CTAS)
     if (go) ctl->taken = taken;
   } else if (warp == 6) {
     // ------------------------------------------------------------ edge rows
-    // Same order of stages as the issuer's, which asks for each group of MT
-    // that needs this warp once it has waited for all stages before it: the
-    // parity waits here cannot mistake an older phase for the stage's own.
-    // lane: 16-byte unit lane % 16 (of the 128 dims) of every second row.
+    // The issuer asks for a V tile that needs this warp once it has waited for
+    // all stages before it: the parity waits here cannot mistake an older phase
+    // for the stage's own. lane: 16-byte unit lane % 16 (of the 128 dims) of
+    // every second row.
     bool ok = n_tiles == 0 || wait_all(&ctl->q_ready, 0, abort_flag, deadline, a.status, 61, 0, 0, 0);
     const int cc = (lane >> 3) & 1, u = lane & 7;
-    int item = 0, groups = 0;
-    // rows of tile j to clear (V), then the new token's row
-    const auto patch = [&](int j, bool isv) {
+    int groups = 0;
+    for (int j = 0; j < n_tiles && ok; ++j) {
       int nb;
       const int p0 = tile(j, &nb);
-      const bool with_new = own_new && j == n_tiles - 1;
-      if (!(isv && is_edge(p0, nb)) && !with_new) {
-        item += MT;
-        return;
-      }
+      if (!is_edge(p0, nb)) continue;
       ok = wait_all(&ctl->patch_req, groups++ & 1, abort_flag, deadline, a.status, 63, j, 0, 0);
       uint32_t off[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        off[q] = __ballot_sync(0xffffffffu, isv && q < nb && !sp.sees(p0 + q * BLK + lane, len_c, a.sinks));
-      const int new_row = len_c - p0;
+        off[q] = __ballot_sync(0xffffffffu, q < nb && !sp.sees(p0 + q * BLK + lane, len_c, a.sinks));
+      const int new_row = own_new && j == n_tiles - 1 ? len_c - p0 : -1;
+      // items: K_0, K_1, V_0, K_2, V_1, ..., V_{n-2}, V_{n-1}
+      int item = MT * (j < n_tiles - 1 ? 2 * j + 2 : 2 * n_tiles - 1);
       for (int h = 0; h < MT && ok; ++h, ++item) {
         const int s = item % NS;
         ok = wait_all(&ctl->full[s], (item / NS) & 1, abort_flag, deadline, a.status, 62, item, s, j);
@@ -437,19 +437,14 @@ __global__ void __launch_bounds__(NT, CTAS)
             }
           }
         __syncwarp();
-        if (with_new && lane < 16)
+        if (new_row >= 0 && lane < 16)
           *reinterpret_cast<uint4*>(st + new_row * 128 + ((u ^ (new_row & 7)) << 4)) =
-              *reinterpret_cast<const uint4*>(newrow + (isv && !a.keqv ? D : 0) + h * 128 + lane * 8);
+              *reinterpret_cast<const uint4*>(newrow + (a.keqv ? 0 : D) + h * 128 + lane * 8);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->patched[s]);
       }
-    };
-    for (int j = 0; j < n_tiles && ok; ++j) {
-      patch(j, false);
-      if (j > 0 && ok) patch(j - 1, true);
     }
-    if (n_tiles > 0 && ok) patch(n_tiles - 1, true);
   } else {
     // ------------------------------------------------------------ rotation, softmax
     const int q4 = warp & 3;
@@ -472,11 +467,30 @@ __global__ void __launch_bounds__(NT, CTAS)
         trig[i] = make_float2(c, s);
       }
       sync128();
+      // The new key's logits are formed here (its row of S is not used): a
+      // thread has 8 dims of some heads and of the key, a warp adds them up.
+      const int c = t128 % CH;
+      float2 kn[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) kn[j] = make_float2(0.f, 0.f);
+      if (own_new) {
+        turn4(*reinterpret_cast<const uint4*>(a.k_new + ((int64_t)b * a.Hkv + g) * D + c * 8), c, a.n_rot, trig, kn);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) kn[j] = unpack_bf16x2(pack_bf16x2(kn[j].x, kn[j].y));  // as the cache holds it
+      }
 #pragma unroll
       for (int k = 0; k < 8 * CH / 128; ++k) {
-        const int i = t128 + k * 128, r = i / CH, c = i % CH;
+        const int r = (t128 + k * 128) / CH;
         float2 y[4];
         turn4(x[k], c, a.n_rot, trig, y);
+        if (own_new) {
+          float dot = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) dot += y[j].x * kn[j].x + y[j].y * kn[j].y;
+#pragma unroll
+          for (int o = 16; o >= 1; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+          if (lane == 0) ctl->s_new[t128 >> 5][r] = dot;
+        }
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -491,15 +505,10 @@ __global__ void __launch_bounds__(NT, CTAS)
       if (own_new && t128 < (a.keqv ? 1 : 2) * CH) {
         const int64_t crow = cache_row(a.page_table, a.pages_per_seq, a.page_size, a.n_pages, a.Hkv, b, g, len - 1);
         if (crow < 0 && t128 == 0) set_status(a.status, GEMMA_ERR_DEVICE_RANGE);
-        const int c = t128 % CH;
         const bool isv = t128 >= CH;
-        uint4 v = *reinterpret_cast<const uint4*>((isv ? a.v_new : a.k_new) + ((int64_t)b * a.Hkv + g) * D + c * 8);
-        if (!isv) {
-          float2 y[4];
-          turn4(v, c, a.n_rot, trig, y);
-          v = make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y), pack_bf16x2(y[2].x, y[2].y),
-                         pack_bf16x2(y[3].x, y[3].y));
-        }
+        uint4 v = make_uint4(pack_bf16x2(kn[0].x, kn[0].y), pack_bf16x2(kn[1].x, kn[1].y),
+                             pack_bf16x2(kn[2].x, kn[2].y), pack_bf16x2(kn[3].x, kn[3].y));
+        if (isv) v = *reinterpret_cast<const uint4*>(a.v_new + ((int64_t)b * a.Hkv + g) * D + c * 8);
         *reinterpret_cast<uint4*>(newrow + (isv ? D : 0) + c * 8) = v;
         if (crow >= 0) *reinterpret_cast<uint4*>((isv ? a.v_pool : a.k_pool) + crow * D + c * 8) = v;
       }
@@ -526,6 +535,13 @@ __global__ void __launch_bounds__(NT, CTAS)
 #pragma unroll
         for (int n = 0; n < 8; ++n)
           v[n] = seen ? (__uint_as_float(r[n]) + __uint_as_float(r[n + 8])) * a.scale_log2 : -INFINITY;
+        if (own_new && p0 + kl == len_c) {
+          // head n's dims lie in the warps with threads of row n: D / 256 of them
+#pragma unroll
+          for (int n = 0; n < 8; ++n)
+            v[n] = (D == 512 ? ctl->s_new[(n & 1) * 2][n] + ctl->s_new[(n & 1) * 2 + 1][n] : ctl->s_new[n & 3][n]) *
+                   a.scale_log2;
+        }
       }
       bool need = bad;
 #pragma unroll
@@ -610,7 +626,7 @@ __global__ void __launch_bounds__(NT, CTAS)
   __syncwarp();
   __syncthreads();
   if (warp == 0 && lane == 0 && *abort_flag) {
-    // loads still in flight must land before shared memory is reused (a
+    // loads still in flight must land before the CTA leaves (a
     // dropped copy, the test hook's, never does: its wait runs out)
     volatile int never = 0;
     const uint64_t dl = globaltimer_ns() + 200000000ull;
@@ -618,9 +634,9 @@ __global__ void __launch_bounds__(NT, CTAS)
       mbar_wait_bounded_at(&ctl->full[i % NS], (i / NS) & 1, &never, dl, a.status, 60, i, i % NS, ctl->taken);
   }
   __syncwarp();
-  pair::cluster_sync();  // every CTA is done with its ring
+  pair::cluster_wait();  // every CTA has begun
   // Each CTA owns D / n_splits output columns; the others push their share of
-  // those into its ring, [split][column][head], and their (m, l).
+  // those into its merge buffer, and their (m, l).
   const int log_n = __ffs(n_splits) - 1, log_cols = (D == 256 ? 8 : 9) - log_n, cols = 1 << log_cols;
   if (warp >= 2 && warp < 6) {
     const int kl = (warp & 3) * 32 + lane;
@@ -640,7 +656,7 @@ __global__ void __launch_bounds__(NT, CTAS)
 #pragma unroll
         for (int n = 0; n < 8; ++n) x[n] = __uint_as_float(o[m][n]) + __uint_as_float(o[m][n + 8]);
         const int d = m * 128 + kl;
-        const uint32_t to = pair::map_to(base, d >> log_cols) + ((split << log_cols) + (d & (cols - 1))) * 32;
+        const uint32_t to = pair::map_to(base + C::MERGE_OFF, d >> log_cols) + ((split << log_cols) + (d & (cols - 1))) * 32;
         st_cluster4(to, x[0], x[1], x[2], x[3]);
         st_cluster4(to + 16, x[4], x[5], x[6], x[7]);
       }
@@ -676,7 +692,7 @@ __global__ void __launch_bounds__(NT, CTAS)
     float x[4] = {0.f, 0.f, 0.f, 0.f};
     for (int s = 0; s < n_splits; ++s) {
       const float4 w = *reinterpret_cast<const float4*>(&ctl->wgt[s][4 * hh]);
-      const float4 v = *reinterpret_cast<const float4*>(sm + ((s << log_cols) + d) * 32 + hh * 16);
+      const float4 v = *reinterpret_cast<const float4*>(sm + C::MERGE_OFF + ((s << log_cols) + d) * 32 + hh * 16);
       // a split without keys pushed nothing
       if (ctl->ml[s][4 * hh].x == -INFINITY) continue;
       x[0] += w.x * v.x;

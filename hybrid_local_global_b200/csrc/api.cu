@@ -294,6 +294,14 @@ int record_error(int code, const char* msg) { return fail(code, "%s", msg); }
 int record_ok() { return succeed(); }
 int* device_status() { return status_ptr(); }
 int multiprocessors() { return sm_count(); }
+void half_turn_ladder(double step, int n, double* out) {
+  double coarse[16], fine[16];
+  for (int i = 0; i < 16; ++i) {
+    coarse[i] = std::exp2(-16.0 * i * step) * 0.31830988618379067153776752674503;  // / pi
+    fine[i] = std::exp2(-i * step);
+  }
+  for (int i = 0; i < n; ++i) out[i] = coarse[i >> 4] * fine[i & 15];
+}
 }  // namespace hlg
 
 extern "C" {

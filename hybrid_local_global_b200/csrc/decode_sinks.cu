@@ -64,7 +64,6 @@ constexpr int BOX_B = BLK * 128;    // one TMA box: 32 keys x 64 dims
 constexpr int P_B = 2 * NQ * 128;   // P^T: two chunks of 64 keys
 constexpr int MAX_CLUSTER = 16;     // CTAs per (sequence, KV head); above 8 where the device allows it
 constexpr float RESCALE_LOG2 = 8.0f;
-constexpr double kInvPi = 0.31830988618379067153776752674503;
 constexpr uint32_t IDESC_ST = tc::idesc_bf16_f32(128, NQ, 0, 0);  // K (K-major) x Q (K-major)
 constexpr uint32_t IDESC_OT = tc::idesc_bf16_f32(128, NQ, 1, 0);  // V^T (MN-major) x P^T (K-major)
 
@@ -796,7 +795,7 @@ cudaError_t launch(const Maps& maps, const SinkDecodeArgs& a, int B, cudaStream_
 }  // namespace
 
 cudaError_t launch_decode_sinks(SinkDecodeArgs& a, int B, int D, double log2_theta, cudaStream_t st) {
-  for (int i = 0; i < a.n_rot; ++i) a.freq[i] = std::exp2(-(2.0 * i / D) * log2_theta) * kInvPi;
+  half_turn_ladder(2.0 / D * log2_theta, a.n_rot, a.freq);
   // (64 dims, row, 64-dim chunk, head, page): a box of 2 chunks is a stage
   const uint64_t ps = (uint64_t)a.page_size, H = (uint64_t)a.Hkv, d = (uint64_t)D;
   const uint64_t dims[5] = {64, ps, d / 64, H, (uint64_t)a.n_pages};

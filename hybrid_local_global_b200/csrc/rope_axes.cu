@@ -135,11 +135,17 @@ extern "C" int gemma_rope_axes(const void* q, long long q_stride, const void* k,
   if (rc) return rc;
 
   AxesArgs a;
+  const double log2_theta = std::log2((double)rope_theta), sign = (flags & GEMMA_ROPE_INVERSE) ? -1.0 : 1.0;
+  double ladder[MAX_AXES][MAX_PAIRS];  // [0]: by the pair's number; with AXIS_LADDERS, of each axis by rank
+  if (flags & GEMMA_ROPE_AXIS_LADDERS) {
+    for (int x = 0; x < n_axes; ++x)
+      if (axis_pairs[x] > 0) half_turn_ladder(log2_theta / axis_pairs[x], axis_pairs[x], ladder[x]);
+  } else {
+    half_turn_ladder(2.0 / head_dim * log2_theta, (int)n_rot, ladder[0]);
+  }
   int i = 0;
   const auto put = [&](int x, int rank) {
-    const double expo = (flags & GEMMA_ROPE_AXIS_LADDERS) ? (double)rank / axis_pairs[x] : 2.0 * i / head_dim;
-    const double f = std::pow((double)rope_theta, -expo) * 0.31830988618379067153776752674503;  // / pi
-    a.freq[i] = (flags & GEMMA_ROPE_INVERSE) ? -f : f;
+    a.freq[i] = sign * ((flags & GEMMA_ROPE_AXIS_LADDERS) ? ladder[x][rank] : ladder[0][i]);
     a.axis[i] = (unsigned char)x;
     ++i;
   };

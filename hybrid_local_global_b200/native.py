@@ -441,76 +441,88 @@ EXPORTED += ["gemma_attn_prefill_sinks", "gemma_attn_decode_sinks_workspace_size
              "gemma_kv_pages_compact", "gemma_kv_pages_copy", "gemma_rope_axes"]
 
 
-def _on(device, stream, what):
-    """The device guard of a call whose tensors are on `device`, and its
-    stream: that device's current one by default."""
-    if device.type != "cuda":
-        raise TypeError("%s: tensors must be on a CUDA device, not %s" % (what, device))
+# These calls may be issued every few microseconds, so their checks use the
+# cheap accessors: get_device() for tensors, the raw current stream.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _on(index, stream, what, call, *args):
+    """`call` with `args` and a stream of device `index` (by default its
+    current one), that device current."""
+    if index < 0:
+        raise TypeError("%s: tensors must be on a CUDA device" % what)
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError("%s: stream of %s, tensors on %s" % (what, stream.device, device))
-    return torch.cuda.device(device), ctypes.c_void_p(stream.cuda_stream)
+        raw = _raw_stream(index)
+    elif stream.device.index == index:
+        raw = stream.cuda_stream
+    else:
+        raise ValueError("%s: stream of %s, tensors on cuda:%d" % (what, stream.device, index))
+    if torch.cuda.current_device() == index:
+        return _check(call(*args, raw))
+    with torch.cuda.device(index):
+        return _check(call(*args, raw))
 
 
-def _need(t, name, dtype, shape, device):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise TypeError("%s must be a contiguous %s tensor on %s" % (name, dtype, device))
-    if tuple(t.shape) != tuple(shape):
+def _need(t, name, dtype, shape, index):
+    """The data pointer of a contiguous tensor of this type, shape and device."""
+    if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        raise TypeError("%s must be a contiguous %s tensor on device %d" % (name, dtype, index))
+    if t.shape != shape:
         raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape), tuple(shape)))
+    return t.data_ptr()
+
+
+_BF16, _I32 = torch.bfloat16, torch.int32
 
 
 def _sinks_args(q, k_new, v_new, k_pool, v_pool, page_table, out, lens, lens_name, flags):
-    """Shapes and devices of a window-plus-sinks call: (B, new token dims, Hq,
-    Hkv, D, page_size, pages_per_seq, n_pages, flags)."""
+    """Shapes and devices of a window-plus-sinks call: its leading C arguments
+    (q .. lens), (B, Hq, Hkv, D, capacity), out's pointer and the flags."""
     if isinstance(k_pool, Int8KVCache) or isinstance(v_pool, Int8KVCache):
-        flags |= _kv_kind(k_pool, v_pool)
-    for t, n in ((q, "q"), (k_new, "k_new"), (v_new, "v_new"), (k_pool, "k_pool"), (v_pool, "v_pool"), (out, "out")):
-        _bf16(t, n)
-    dev = q.device
-    B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
-    n_pages, Hkv, ps, pps = _paged_args(k_pool, page_table)
-    _need(page_table, "page_table", torch.int32, (B, pps), dev)
-    if k_pool.shape[-1] != D or (v_pool is not None and tuple(v_pool.shape) != tuple(k_pool.shape)):
-        raise ValueError("k_pool and v_pool must be [n_pages, Hkv, page_size, D] with the D of q")
-    for t, n in ((k_pool, "k_pool"), (v_pool, "v_pool")):
-        if t is not None and t.device != dev:
-            raise TypeError("%s is on %s, q on %s" % (n, t.device, dev))
-    for t, n in ((k_new, "k_new"), (v_new, "v_new")):
-        if t is not None:
-            _need(t, n, torch.bfloat16, (*q.shape[:-2], Hkv, D), dev)
-    _need(out, "out", torch.bfloat16, q.shape, dev)
-    if lens is not None:
-        _need(lens, lens_name, torch.int32, (B,), dev)
-    return B, Hq, Hkv, D, ps, pps, n_pages, flags
+        flags |= _kv_kind(k_pool, v_pool)  # refused below, by the library
+        pools = (k_pool.data_ptr(), None if v_pool is None else v_pool.data_ptr())
+    else:
+        pools = None
+    i = q.get_device()
+    qs = q.shape
+    B, Hq, D = qs[0], qs[-2], qs[-1]
+    if len(k_pool.shape) != 4 or k_pool.shape[3] != D:
+        raise ValueError("k_pool must be [n_pages, Hkv, page_size, D] with the D of q")
+    n_pages, Hkv, ps, _ = shape = tuple(k_pool.shape)
+    if pools is None:
+        pools = (_need(k_pool, "k_pool", _BF16, shape, i),
+                 None if v_pool is None else _need(v_pool, "v_pool", _BF16, shape, i))
+    pps = page_table.shape[-1]
+    new = (*qs[:-2], Hkv, D)
+    args = (_need(q, "q", _BF16, qs, i), None if k_new is None else _need(k_new, "k_new", _BF16, new, i),
+            None if v_new is None else _need(v_new, "v_new", _BF16, new, i), *pools,
+            _need(page_table, "page_table", _I32, (B, pps), i), ps, pps, n_pages,
+            None if lens is None else _need(lens, lens_name, _I32, (B,), i))
+    return i, args, (B, Hq, Hkv, D), _need(out, "out", _BF16, qs, i), flags
 
 
-def _workspace(workspace, size, device):
+def _workspace(workspace, size, index):
+    """(pointer, bytes) of the caller's workspace, or of one of size() bytes."""
     if workspace is None:
-        return torch.empty(max(size, 1), dtype=torch.uint8, device=device)
-    if workspace.device != device or not workspace.is_contiguous():
-        raise TypeError("workspace must be a contiguous tensor on %s" % device)
-    return workspace
+        workspace = torch.empty(max(size(), 1), dtype=torch.uint8, device="cuda:%d" % index)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous tensor on device %d" % index)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def gemma_attn_prefill_sinks(q, k_new, v_new, k_pool, v_pool, page_table, *, window, sinks, rope_frac, rope_theta,
                              scale, out, seq_lens_before=None, lse=None, workspace=None, flags=0, stream=None):
     """A chunk on a paged layer that sees the last `window` positions and the
     first `sinks`: tensors as gemma_attn_prefill_paged (bf16 pools)."""
-    B, Hq, Hkv, D, ps, pps, n_pages, flags = _sinks_args(q, k_new, v_new, k_pool, v_pool, page_table, out,
-                                                         seq_lens_before, "seq_lens_before", flags)
-    S = q.shape[1]
     if q.dim() != 4:
         raise ValueError("q must be [B, S, Hq, D]")
-    if lse is not None:
-        _need(lse, "lse", torch.float32, (B, Hq, S), q.device)
-    workspace = _workspace(workspace, gemma_attn_prefill_workspace_size(B, S, Hq, Hkv, D, 0), q.device)
-    guard, st = _on(q.device, stream, "gemma_attn_prefill_sinks")
-    with guard:
-        return _check(_prefill_sinks(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool), _ptr(v_pool), _ptr(page_table),
-                                     ps, pps, n_pages, _ptr(seq_lens_before), B, S, window, sinks, Hq, Hkv, D,
-                                     rope_frac, rope_theta, scale, _ptr(out), _ptr(lse), _ptr(workspace),
-                                     workspace.numel() * workspace.element_size(), flags, st))
+    i, args, (B, Hq, Hkv, D), out_p, flags = _sinks_args(q, k_new, v_new, k_pool, v_pool, page_table, out,
+                                                         seq_lens_before, "seq_lens_before", flags)
+    S = q.shape[1]
+    lse_p = None if lse is None else _need(lse, "lse", torch.float32, (B, Hq, S), i)
+    keep, ws, ws_bytes = _workspace(workspace, lambda: gemma_attn_prefill_workspace_size(B, S, Hq, Hkv, D, 0), i)
+    return _on(i, stream, "gemma_attn_prefill_sinks", _prefill_sinks, *args, B, S, window, sinks, Hq, Hkv, D, rope_frac,
+               rope_theta, scale, out_p, lse_p, ws, ws_bytes, flags)
 
 
 def gemma_attn_decode_sinks_workspace_size(batch, n_q_heads, n_kv_heads, head_dim, window, sinks, max_seq_len) -> int:
@@ -524,18 +536,14 @@ def gemma_attn_decode_sinks(q, k_new, v_new, k_pool, v_pool, page_table, *, seq_
     pools); seq_lens 0 marks an idle slot."""
     if seq_lens is None:
         raise TypeError("seq_lens is required")
-    B, Hq, Hkv, D, ps, pps, n_pages, flags = _sinks_args(q, k_new, v_new, k_pool, v_pool, page_table, out, seq_lens,
-                                                         "seq_lens", flags)
     if q.dim() != 3:
         raise ValueError("q must be [B, Hq, D]")
-    workspace = _workspace(workspace, gemma_attn_decode_sinks_workspace_size(B, Hq, Hkv, D, window, sinks, max_seq_len),
-                           q.device)
-    guard, st = _on(q.device, stream, "gemma_attn_decode_sinks")
-    with guard:
-        return _check(_decode_sinks(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool), _ptr(v_pool), _ptr(page_table),
-                                    ps, pps, n_pages, _ptr(seq_lens), max_seq_len, B, window, sinks, Hq, Hkv, D,
-                                    rope_frac, rope_theta, scale, _ptr(out), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), flags, st))
+    i, args, (B, Hq, Hkv, D), out_p, flags = _sinks_args(q, k_new, v_new, k_pool, v_pool, page_table, out, seq_lens,
+                                                         "seq_lens", flags)
+    keep, ws, ws_bytes = _workspace(
+        workspace, lambda: gemma_attn_decode_sinks_workspace_size(B, Hq, Hkv, D, window, sinks, max_seq_len), i)
+    return _on(i, stream, "gemma_attn_decode_sinks", _decode_sinks, *args, max_seq_len, B, window, sinks, Hq, Hkv, D,
+               rope_frac, rope_theta, scale, out_p, ws, ws_bytes, flags)
 
 
 class PageBook:
@@ -551,41 +559,28 @@ class PageBook:
         self.ref_count = self.state[n:]
         self.page_table.fill_(-1)
         self.page_size = page_size
+        self.n_seqs, self.pages_per_seq, self.n_pages = n_seqs, pages_per_seq, n_pages
         self.device = self.state.device
         self.desc = gemma_page_book(self.page_table.data_ptr(), self.ref_count.data_ptr(), n_seqs, pages_per_seq,
                                     n_pages, page_size)
-
-    @property
-    def n_seqs(self):
-        return self.page_table.shape[0]
-
-    @property
-    def pages_per_seq(self):
-        return self.page_table.shape[1]
-
-    @property
-    def n_pages(self):
-        return self.ref_count.shape[0]
+        self._ref = ctypes.byref(self.desc)
+        self._index = self.state.get_device()
 
 
-def _book(book):
-    return ctypes.byref(book.desc)
-
-
-def _pool_list(pools, n_pages, page_size, device):
+def _pool_list(pools, n_pages, page_size, index):
     """gemma_page_pool array of bf16 tensors [n_pages, Hkv, page_size, D] and
     Int8KVCache(n_pages, Hkv, page_size, D) buffers."""
-    arr = (gemma_page_pool * max(len(pools), 1))()
-    for i, p in enumerate(pools):
+    rows = []
+    for p in pools:
         q8 = isinstance(p, Int8KVCache)
-        _bf16(p, "pool")
-        if len(p.shape) != 4 or p.shape[0] != n_pages or p.shape[2] != page_size:
-            raise ValueError("pool %d must be [n_pages %d, Hkv, page_size %d, D]" % (i, n_pages, page_size))
-        if p.device != device:
-            raise TypeError("pool %d is on %s, not %s" % (i, p.device, device))
-        arr[i].pool, arr[i].n_kv_heads, arr[i].head_dim = p.data_ptr(), p.shape[1], p.shape[3]
-        arr[i].flags = GEMMA_F_KV_INT8 if q8 else 0
-    return arr
+        shape = p.shape
+        if len(shape) != 4 or shape[0] != n_pages or shape[2] != page_size:
+            raise ValueError("pool %d must be [n_pages %d, Hkv, page_size %d, D]" % (len(rows), n_pages, page_size))
+        t = p.buf if q8 else p
+        if t.get_device() != index or not (q8 or (t.dtype is _BF16 and t.is_contiguous())):
+            raise TypeError("pool %d must be a contiguous bf16 tensor or an Int8KVCache on device %d" % (len(rows), index))
+        rows.append((t.data_ptr(), shape[1], shape[3], GEMMA_F_KV_INT8 if q8 else 0))
+    return (gemma_page_pool * max(len(rows), 1))(*rows)
 
 
 def gemma_kv_pages_workspace_size(n_seqs, pages_per_seq, n_pages) -> int:
@@ -594,83 +589,78 @@ def gemma_kv_pages_workspace_size(n_seqs, pages_per_seq, n_pages) -> int:
 
 def gemma_kv_pages_fork(book, parents, *, stream=None):
     """Row b of the book's table becomes row parents[b] (int32 [n_seqs]; b: unchanged, -1: empty)."""
-    _need(parents, "parents", torch.int32, (book.n_seqs,), book.device)
-    guard, st = _on(book.device, stream, "gemma_kv_pages_fork")
-    with guard:
-        return _check(_pages_fork(_book(book), _ptr(parents), st))
+    i = book._index
+    return _on(i, stream, "gemma_kv_pages_fork", _pages_fork, book._ref,
+               _need(parents, "parents", _I32, (book.n_seqs,), i))
+
+
+def _book_workspace(book, workspace):
+    return _workspace(workspace,
+                      lambda: gemma_kv_pages_workspace_size(book.n_seqs, book.pages_per_seq, book.n_pages), book._index)
 
 
 def gemma_kv_pages_reserve(book, pools, *, seq_lens, new_tokens, lacking, workspace=None, stream=None):
     """Grants pages (copying shared ones that will be written) for positions
     seq_lens[b] .. + new_tokens[b] of every row; lacking int32 [1] receives
     how many pages are missing (then nothing was changed)."""
-    dev = book.device
-    _need(seq_lens, "seq_lens", torch.int32, (book.n_seqs,), dev)
-    _need(new_tokens, "new_tokens", torch.int32, (book.n_seqs,), dev)
-    _need(lacking, "lacking", torch.int32, (1,), dev)
-    arr = _pool_list(pools, book.n_pages, book.page_size, dev)
-    workspace = _workspace(workspace, gemma_kv_pages_workspace_size(book.n_seqs, book.pages_per_seq, book.n_pages), dev)
-    guard, st = _on(dev, stream, "gemma_kv_pages_reserve")
-    with guard:
-        return _check(_pages_reserve(_book(book), arr, len(pools), _ptr(seq_lens), _ptr(new_tokens), _ptr(lacking),
-                                     _ptr(workspace), workspace.numel() * workspace.element_size(), st))
+    i, n = book._index, (book.n_seqs,)
+    lens, new = _need(seq_lens, "seq_lens", _I32, n, i), _need(new_tokens, "new_tokens", _I32, n, i)
+    short = _need(lacking, "lacking", _I32, (1,), i)
+    arr = _pool_list(pools, book.n_pages, book.page_size, i)
+    keep, ws, ws_bytes = _book_workspace(book, workspace)
+    return _on(i, stream, "gemma_kv_pages_reserve", _pages_reserve, book._ref, arr, len(pools), lens, new, short, ws,
+               ws_bytes)
 
 
 def gemma_kv_pages_trim(book, *, seq_lens, window=0, sinks=0, stream=None):
     """Drops the pages that hold nothing a token after seq_lens[b] sees
     (int32 [n_seqs]; 0 ends the sequence, below 0 leaves its row alone)."""
-    _need(seq_lens, "seq_lens", torch.int32, (book.n_seqs,), book.device)
-    guard, st = _on(book.device, stream, "gemma_kv_pages_trim")
-    with guard:
-        return _check(_pages_trim(_book(book), _ptr(seq_lens), window, sinks, st))
+    i = book._index
+    return _on(i, stream, "gemma_kv_pages_trim", _pages_trim, book._ref,
+               _need(seq_lens, "seq_lens", _I32, (book.n_seqs,), i), window, sinks)
 
 
 def gemma_kv_pages_compact(book, pools, *, n_live, page_map=None, workspace=None, stream=None):
     """Moves the live pages to numbers 0 .. n_live - 1 (n_live int32 [1],
     written); page_map int32 [n_pages]: the new number of every live page."""
-    dev = book.device
-    _need(n_live, "n_live", torch.int32, (1,), dev)
-    if page_map is not None:
-        _need(page_map, "page_map", torch.int32, (book.n_pages,), dev)
-    arr = _pool_list(pools, book.n_pages, book.page_size, dev)
-    workspace = _workspace(workspace, gemma_kv_pages_workspace_size(book.n_seqs, book.pages_per_seq, book.n_pages), dev)
-    guard, st = _on(dev, stream, "gemma_kv_pages_compact")
-    with guard:
-        return _check(_pages_compact(_book(book), arr, len(pools), _ptr(n_live), _ptr(page_map), _ptr(workspace),
-                                     workspace.numel() * workspace.element_size(), st))
+    i = book._index
+    live = _need(n_live, "n_live", _I32, (1,), i)
+    names = None if page_map is None else _need(page_map, "page_map", _I32, (book.n_pages,), i)
+    arr = _pool_list(pools, book.n_pages, book.page_size, i)
+    keep, ws, ws_bytes = _book_workspace(book, workspace)
+    return _on(i, stream, "gemma_kv_pages_compact", _pages_compact, book._ref, arr, len(pools), live, names, ws, ws_bytes)
 
 
 def gemma_kv_pages_copy(pools, *, src, dst, stream=None):
     """Copies pages src[i] -> dst[i] (int32 [n]) in every pool of the list."""
     if not pools:
         raise ValueError("no pools")
-    dev = pools[0].device
     n_pages, _, page_size, _ = pools[0].shape
     if src.dim() != 1:
         raise ValueError("src must be one-dimensional")
-    _need(src, "src", torch.int32, src.shape, dev)
-    _need(dst, "dst", torch.int32, src.shape, dev)
-    arr = _pool_list(pools, n_pages, page_size, dev)
-    guard, st = _on(dev, stream, "gemma_kv_pages_copy")
-    with guard:
-        return _check(_pages_copy(arr, len(pools), n_pages, page_size, _ptr(src), _ptr(dst), src.numel(), st))
+    i = src.get_device()
+    src_p, dst_p = _need(src, "src", _I32, src.shape, i), _need(dst, "dst", _I32, src.shape, i)
+    arr = _pool_list(pools, n_pages, page_size, i)
+    return _on(i, stream, "gemma_kv_pages_copy", _pages_copy, arr, len(pools), n_pages, page_size, src_p, dst_p,
+               src.shape[0])
 
 
-def _token_rows(t, name, heads_dim):
-    """(token stride, heads) of [..., heads, D] whose heads are dense and whose
-    leading dimensions step evenly."""
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() < 3:
-        raise TypeError("%s must be a bf16 CUDA tensor [..., heads, head_dim]" % name)
-    H, D = t.shape[-2:]
-    if D != heads_dim:
-        raise ValueError("%s has head_dim %d, not %d" % (name, D, heads_dim))
-    lead = [(n, s) for n, s in zip(t.shape[:-2], t.stride()[:-2]) if n != 1]
-    ok = t.numel() == 0 or ((D == 1 or t.stride(-1) == 1) and (H == 1 or t.stride(-2) == D))
-    for (_, s0), (n1, s1) in zip(lead, lead[1:]):
-        ok = ok and s0 == n1 * s1
-    if not ok and t.numel():
+def _token_stride(t, name, tokens, D, index):
+    """Elements between tokens of a bf16 tensor [..., heads, D] of this token
+    shape, whose heads are dense and whose tokens are evenly spaced."""
+    shape = t.shape
+    if t.dtype is not _BF16 or t.get_device() != index:
+        raise TypeError("%s must be a bf16 tensor on device %d" % (name, index))
+    if shape[:-2] != tokens or shape[-1] != D:
+        raise ValueError("%s has shape %s: tokens %s and head_dim %d expected" % (name, tuple(shape), tuple(tokens), D))
+    if t.is_contiguous():
+        return shape[-2] * D
+    stride = t.stride()
+    lead = [(n, s) for n, s in zip(tokens, stride) if n != 1]
+    if stride[-1] != 1 or (shape[-2] != 1 and stride[-2] != D) or any(
+            s0 != n1 * s1 for (_, s0), (n1, s1) in zip(lead, lead[1:])):
         raise ValueError("%s: heads must be dense and tokens evenly spaced" % name)
-    return (lead[-1][1] if lead else H * D), H
+    return lead[-1][1] if lead else shape[-2] * D
 
 
 def gemma_rope_axes(q, k, positions, *, axis_pairs, rope_theta, q_out, k_out=None, flags=0, stream=None):
@@ -678,28 +668,24 @@ def gemma_rope_axes(q, k, positions, *, axis_pairs, rope_theta, q_out, k_out=Non
     (or None) turned by positions int32 [n_axes, ...] into q_out and k_out
     (which may be q and k). Tokens may be strided, e.g. slices of a fused
     projection; see GEMMA_ROPE_* for flags."""
-    D = q.shape[-1]
-    qs, Hq = _token_rows(q, "q", D)
-    qos, _ = _token_rows(q_out, "q_out", D)
-    tokens = math.prod(q.shape[:-2])
+    if q.dim() < 3:
+        raise ValueError("q must be [..., heads, head_dim]")
+    i = q.get_device()
+    lead, Hq, D = q.shape[:-2], q.shape[-2], q.shape[-1]
     if q_out.shape != q.shape:
         raise ValueError("q_out must have the shape of q")
+    qs, qos = _token_stride(q, "q", lead, D, i), _token_stride(q_out, "q_out", lead, D, i)
     ks = kos = Hkv = 0
+    k_p = ko_p = None
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
     if k is not None:
-        ks, Hkv = _token_rows(k, "k", D)
-        kos, _ = _token_rows(k_out, "k_out", D)
-        if k.shape[:-2] != q.shape[:-2] or k_out.shape != k.shape:
-            raise ValueError("k and k_out must have the tokens of q")
-    dev = q.device
-    for t, n in ((q_out, "q_out"), (k, "k"), (k_out, "k_out")):
-        if t is not None and t.device != dev:
-            raise TypeError("%s is on %s, q on %s" % (n, t.device, dev))
+        if k_out.shape != k.shape:
+            raise ValueError("k_out must have the shape of k")
+        ks, kos = _token_stride(k, "k", lead, D, i), _token_stride(k_out, "k_out", lead, D, i)
+        Hkv, k_p, ko_p = k.shape[-2], k.data_ptr(), k_out.data_ptr()
     n_axes = len(axis_pairs)
-    _need(positions, "positions", torch.int32, (n_axes, *q.shape[:-2]), dev)
-    pairs = (_I * max(n_axes, 1))(*axis_pairs)
-    guard, st = _on(dev, stream, "gemma_rope_axes")
-    with guard:
-        return _check(_rope_axes(_ptr(q), qs, _ptr(k), ks, _ptr(positions), n_axes, pairs, tokens, Hq, Hkv, D,
-                                 rope_theta, _ptr(q_out), qos, _ptr(k_out), kos, flags, st))
+    pos = _need(positions, "positions", _I32, (n_axes, *lead), i)
+    return _on(i, stream, "gemma_rope_axes", _rope_axes, q.data_ptr(), qs, k_p, ks, pos, n_axes,
+               (_I * max(n_axes, 1))(*axis_pairs), math.prod(lead), Hq, Hkv, D, rope_theta, q_out.data_ptr(), qos, ko_p,
+               kos, flags)

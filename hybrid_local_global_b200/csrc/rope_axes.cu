@@ -14,9 +14,10 @@
 // sine and cosine of the reduced angle and the rotation are fp32, and the
 // result is rounded to bf16 once.
 //
-// Bound by HBM: every vector is read and written once. The angles of a token
-// are the same for all of its heads, so a CTA forms them once per token in
-// shared memory.
+// Bound by HBM: every vector is read and written once. A thread owns 8 elements
+// (4 pairs) of a token's head vectors, so its angles are formed once per token,
+// stay in registers and serve all heads, which it loads eight at a time (two
+// at a time, and the heads dealt to several CTAs, for a few tokens).
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
@@ -44,41 +45,60 @@ struct AxesArgs {
   int tokens, Hq, Hkv, D, n_rot;
 };
 
-// grid.x strides over tokens. Thread (c, r): 8 elements c of head vectors
-// r, r + R, ... of the token.
-__global__ void __launch_bounds__(AX_T) k_rope_axes(const __grid_constant__ AxesArgs a) {
-  __shared__ float2 trig[MAX_PAIRS];
+// Thread (c, y): elements 8c .. of token blockIdx.x * R + y; blockIdx.y: one of
+// gridDim.y shares of the heads. U: head vectors loaded before the first store
+// (8 with three CTAs per SM: 71 us for 8192 tokens of 48 heads of 256, 86 % of the
+// copy rate; 4 with four: 72, 12 with two: 81; and for 19881 tokens of 32 heads
+// of 64: 30, 34, 37).
+template <int U>
+__global__ void __launch_bounds__(AX_T, 3) k_rope_axes(const __grid_constant__ AxesArgs a) {
   const int C = a.D / 8, R = AX_T / C;
-  const int c = threadIdx.x % C, r = threadIdx.x / C;
-  const int H = a.Hq + a.Hkv;
-  for (int t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-    __syncthreads();  // the previous token's angles have been read
-    for (int i = threadIdx.x; i < a.n_rot; i += AX_T) {
-      const double x = (double)a.pos[(int64_t)a.axis[i] * a.tokens + t] * a.freq[i];
-      float s, co;
-      sincospif((float)(x - 2.0 * rint(0.5 * x)), &s, &co);
-      trig[i] = make_float2(co, s);
-    }
-    __syncthreads();
-    if (r >= R) continue;
-    float2 cs[4];
+  const int c = threadIdx.x % C, y = threadIdx.x / C;
+  const int64_t t = (int64_t)blockIdx.x * R + y;
+  if (y >= R || t >= a.tokens) return;
+  const int turning = a.n_rot - c * 4;  // of this thread's four pairs, the first `turning` turn
+  float co[4], sn[4];
+  bool formed = false;
+  const auto stream = [&](const bf16* src, bf16* dst, int heads) {
+    if (turning <= 0 && src == dst) return;  // stays as it is
+    for (int h0 = 0; h0 < heads; h0 += U) {
+      uint4 v[U];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) cs[j] = c * 4 + j < a.n_rot ? trig[c * 4 + j] : make_float2(1.f, 0.f);
-    for (int h = r; h < H; h += R) {
-      const bool is_q = h < a.Hq;
-      const bf16* src = is_q ? a.q + t * a.q_stride + h * a.D : a.k + t * a.k_stride + (h - a.Hq) * a.D;
-      bf16* dst = is_q ? a.q_out + t * a.q_out_stride + h * a.D : a.k_out + t * a.k_out_stride + (h - a.Hq) * a.D;
-      uint4 v = *reinterpret_cast<const uint4*>(src + c * 8);
-      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int u = 0; u < U; ++u)
+        if (h0 + u < heads) v[u] = __ldcs(reinterpret_cast<const uint4*>(src + (int64_t)(h0 + u) * a.D));
+      if (turning <= 0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (c * 4 + j < a.n_rot) {
-          const float2 x = unpack_bf16x2(w[j]);
-          w[j] = pack_bf16x2(x.x * cs[j].x - x.y * cs[j].y, x.x * cs[j].y + x.y * cs[j].x);
+        for (int u = 0; u < U; ++u)
+          if (h0 + u < heads) *reinterpret_cast<uint4*>(dst + (int64_t)(h0 + u) * a.D) = v[u];
+        continue;
+      }
+      if (!formed) {  // while the first vectors are on their way
+        formed = true;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = c * 4 + (j < turning ? j : 0);
+          const double x = (double)a.pos[(int64_t)a.axis[i] * a.tokens + t] * a.freq[i];
+          sincospif((float)(x - 2.0 * rint(0.5 * x)), &sn[j], &co[j]);
         }
-      *reinterpret_cast<uint4*>(dst + c * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = unpack_bf16x2(w[j]);
+          const uint32_t z = pack_bf16x2(x.x * co[j] - x.y * sn[j], x.x * sn[j] + x.y * co[j]);
+          w[j] = j < turning ? z : w[j];
+        }
+        if (h0 + u < heads) *reinterpret_cast<uint4*>(dst + (int64_t)(h0 + u) * a.D) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
-  }
+  };
+  const int64_t share = blockIdx.y, shares = gridDim.y;
+  const int q0 = (int)(a.Hq * share / shares), q1 = (int)(a.Hq * (share + 1) / shares);
+  const int k0 = (int)(a.Hkv * share / shares), k1 = (int)(a.Hkv * (share + 1) / shares), e = c * 8;
+  stream(a.q + t * a.q_stride + q0 * a.D + e, a.q_out + t * a.q_out_stride + q0 * a.D + e, q1 - q0);
+  if (k1 > k0) stream(a.k + t * a.k_stride + k0 * a.D + e, a.k_out + t * a.k_out_stride + k0 * a.D + e, k1 - k0);
 }
 
 int err(int code, const char* msg) { return record_error(code, msg); }
@@ -171,8 +191,14 @@ extern "C" int gemma_rope_axes(const void* q, long long q_stride, const void* k,
   a.Hq = n_q_heads;
   a.Hkv = n_kv_heads;
   a.D = head_dim;
-  const int grid = std::min(tokens, multiprocessors() * 8);
-  k_rope_axes<<<grid, AX_T, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  const int per_cta = AX_T / (head_dim / 8), ctas = (tokens + per_cta - 1) / per_cta;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (ctas >= multiprocessors()) {
+    k_rope_axes<8><<<ctas, AX_T, 0, st>>>(a);
+  } else {  // few tokens: two head vectors of a thread, the others in more CTAs
+    const int shares = std::min((n_q_heads + n_kv_heads + 1) / 2, 65535);
+    k_rope_axes<2><<<dim3(ctas, shares), AX_T, 0, st>>>(a);
+  }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     char m[256];

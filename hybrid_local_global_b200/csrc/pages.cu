@@ -18,6 +18,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "pair.cuh"
 
 namespace hlg {
 
@@ -26,7 +27,9 @@ namespace {
 constexpr int MAX_SEQS = 4096;       // rows of a book (row offsets and fork columns live in shared memory)
 constexpr int MAX_PAGES = 1 << 20;   // pages of a book (compaction keeps one bit per page in shared memory)
 constexpr int MAX_SEGS = 128;        // page segments per copy launch (an int8 pool has two: codes, params)
+constexpr int FEW_SEGS = 8;
 constexpr int PLAN_T = 1024;
+constexpr int SMALL_CTAS = 8;        // CTAs of a one-launch reserve
 constexpr int COPY_T = 256;
 constexpr int COPY_V = 4;            // 16-byte words per thread and tile
 constexpr int TILE_B = COPY_T * COPY_V * 16;
@@ -146,9 +149,9 @@ __device__ __forceinline__ int row_of(const int* off, int n_seqs, int i) {
   return lo;
 }
 
-__global__ void __launch_bounds__(PLAN_T) k_pages_reserve(Book bk, const int32_t* __restrict__ seq_lens,
-                                                          const int32_t* __restrict__ new_tokens,
-                                                          int32_t* lacking, ReservePlan ws, int* status) {
+__device__ __forceinline__ void reserve_plan(const Book& bk, const int32_t* __restrict__ seq_lens,
+                                             const int32_t* __restrict__ new_tokens, int32_t* lacking,
+                                             const ReservePlan& ws, int* status) {
   __shared__ int off[MAX_SEQS];  // first slot of each row
   __shared__ int s_copies;
   const int tid = threadIdx.x;
@@ -264,6 +267,12 @@ __global__ void __launch_bounds__(PLAN_T) k_pages_reserve(Book bk, const int32_t
   }
 }
 
+__global__ void __launch_bounds__(PLAN_T) k_pages_reserve(Book bk, const int32_t* __restrict__ seq_lens,
+                                                          const int32_t* __restrict__ new_tokens,
+                                                          int32_t* lacking, ReservePlan ws, int* status) {
+  reserve_plan(bk, seq_lens, new_tokens, lacking, ws, status);
+}
+
 // ---------------------------------------------------------------------------
 // Compact: with n live pages, the k-th live page numbered n or more moves into
 // the k-th free page numbered below n.
@@ -324,19 +333,6 @@ __global__ void __launch_bounds__(PLAN_T) k_pages_compact(Book bk, CompactPlan w
   }
 }
 
-__global__ void __launch_bounds__(256) k_pages_rename(Book bk, const int32_t* __restrict__ map, int* status) {
-  const int64_t n = (int64_t)bk.n_seqs * bk.pps;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int32_t e = bk.table[i];
-    if (e == -1) continue;
-    const int32_t to = e >= 0 && e < bk.n_pages ? map[e] : -1;
-    if (to < 0)
-      set_status(status, GEMMA_ERR_DEVICE_RANGE);  // an entry that names no live page stays as it is
-    else if (to != e)
-      bk.table[i] = to;
-  }
-}
-
 // ---------------------------------------------------------------------------
 // Page contents
 // ---------------------------------------------------------------------------
@@ -345,12 +341,11 @@ __global__ void __launch_bounds__(256) k_pages_rename(Book bk, const int32_t* __
 struct Seg {
   unsigned char* base;
   long long page_bytes;
-  int heads, head_bytes, row_bytes;
+  int head_bytes, row_bytes;
   int tiles_per_head, tile0;  // tiles of TILE_B bytes; the segment's first tile of a page
 };
 
-struct CopyArgs {
-  Seg seg[MAX_SEGS];
+struct CopyList {
   int n_segs, tiles;          // tiles per page over all segments
   const int32_t* src;         // pair k: src[k * stride], dst[k * stride], rows[k * stride] (null: whole pages)
   const int32_t* dst;
@@ -362,15 +357,21 @@ struct CopyArgs {
   int check;                  // 1: the caller's own list: see pair_ok
   int* status;
 };
+// Two sizes: most calls list a few pools, and a launch copies its parameters.
+template <int N>
+struct CopyArgs {
+  CopyList list;
+  Seg seg[N];
+};
 
 // A listed pair is carried out iff both pages exist, differ, no other pair
 // names the same destination, and no other pair writes its source; the answer
 // depends on the list alone. Called by the whole CTA.
-__device__ __forceinline__ bool pair_ok(const CopyArgs& a, int k, int n) {
+__device__ __forceinline__ bool pair_ok(const CopyList& a, int k, int n) {
   const int32_t s = a.src[k], d = a.dst[k];
   if (s == d && s >= 0 && s < a.n_pages) return false;  // nothing to do, unless another pair names it
   bool bad = s < 0 || s >= a.n_pages || d < 0 || d >= a.n_pages;
-  for (int j = threadIdx.x; j < n; j += COPY_T) {
+  for (int j = threadIdx.x; j < n; j += blockDim.x) {
     if (j == k) continue;
     const int32_t dj = a.dst[j];
     bad |= dj == d || (dj == s && a.src[j] != dj);
@@ -380,12 +381,17 @@ __device__ __forceinline__ bool pair_ok(const CopyArgs& a, int k, int n) {
   return false;
 }
 
-__global__ void __launch_bounds__(COPY_T) k_pages_copy(const __grid_constant__ CopyArgs a) {
+// CTA `cta` of `ctas` copies its share of the list's tiles, T threads of
+// COPY_V words each.
+template <int T>
+__device__ __forceinline__ void copy_tiles(const CopyList& a, const Seg* seg, int cta, int ctas) {
+  constexpr int TILE = T * COPY_V * 16, PER = TILE / TILE_B;  // the list counts tiles of TILE_B bytes
+  static_assert(TILE % TILE_B == 0, "whole tiles");
   const int n = a.n_dev ? *a.n_dev : a.n_host;
   int checked = -1;
   bool ok = true;
-  for (int64_t w = blockIdx.x; w < (int64_t)n * a.tiles; w += gridDim.x) {
-    const int k = (int)(w / a.tiles), t = (int)(w % a.tiles);
+  for (int64_t w = cta; w < (int64_t)n * a.tiles; w += ctas) {
+    const int k = (int)(w / a.tiles), t = (int)(w - (int64_t)k * a.tiles);
     if (a.check && checked != k) {
       ok = pair_ok(a, k, n);
       checked = k;
@@ -394,13 +400,14 @@ __global__ void __launch_bounds__(COPY_T) k_pages_copy(const __grid_constant__ C
     int lo = 0, hi = a.n_segs - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (a.seg[mid].tile0 <= t) lo = mid;
+      if (seg[mid].tile0 <= t) lo = mid;
       else hi = mid - 1;
     }
-    const Seg& g = a.seg[lo];
-    const int head = (t - g.tile0) / g.tiles_per_head, tile = (t - g.tile0) % g.tiles_per_head;
+    const Seg& g = seg[lo];
+    const int head = (t - g.tile0) / g.tiles_per_head, tile = (t - g.tile0) - head * g.tiles_per_head;
+    if (tile % PER) continue;
     const int rows = a.rows ? a.rows[(int64_t)k * a.stride] : a.ps;
-    const int bytes = min(rows * g.row_bytes - tile * TILE_B, TILE_B);
+    const int bytes = min(rows * g.row_bytes - tile * TILE_B, TILE);
     if (bytes <= 0) continue;
     const int64_t at = (int64_t)head * g.head_bytes + (int64_t)tile * TILE_B;
     const unsigned char* from = g.base + a.src[(int64_t)k * a.stride] * g.page_bytes + at;
@@ -408,17 +415,49 @@ __global__ void __launch_bounds__(COPY_T) k_pages_copy(const __grid_constant__ C
     uint4 v[COPY_V];
 #pragma unroll
     for (int u = 0; u < COPY_V; ++u) {
-      const int o = (u * COPY_T + threadIdx.x) * 16;
+      const int o = (u * T + threadIdx.x) * 16;
       if (o + 16 <= bytes) v[u] = *reinterpret_cast<const uint4*>(from + o);
     }
 #pragma unroll
     for (int u = 0; u < COPY_V; ++u) {
-      const int o = (u * COPY_T + threadIdx.x) * 16;
+      const int o = (u * T + threadIdx.x) * 16;
       if (o + 16 <= bytes) *reinterpret_cast<uint4*>(to + o) = v[u];
       else if (o < bytes)  // an odd number of 8-byte (min, step) rows
         *reinterpret_cast<uint2*>(to + o) = *reinterpret_cast<const uint2*>(from + o);
     }
   }
+}
+
+// The copies of a list; with `map`, first the entries of the book's table by
+// their pages' new names.
+template <int N>
+__global__ void __launch_bounds__(COPY_T) k_pages_copy(const __grid_constant__ CopyArgs<N> a, const Book bk,
+                                                       const int32_t* __restrict__ map) {
+  if (map) {
+    const int64_t n = (int64_t)bk.n_seqs * bk.pps;
+    for (int64_t i = (int64_t)blockIdx.x * COPY_T + threadIdx.x; i < n; i += (int64_t)gridDim.x * COPY_T) {
+      const int32_t e = bk.table[i];
+      if (e == -1) continue;
+      const int32_t to = e >= 0 && e < bk.n_pages ? map[e] : -1;
+      if (to < 0)
+        set_status(a.list.status, GEMMA_ERR_DEVICE_RANGE);  // an entry that names no live page stays as it is
+      else if (to != e)
+        bk.table[i] = to;
+    }
+  }
+  copy_tiles<COPY_T>(a.list, a.seg, blockIdx.x, gridDim.x);
+}
+
+// Reserve in one launch, where few bytes can be copied at most: one cluster,
+// whose first CTA makes the plan.
+template <int N>
+__global__ void __cluster_dims__(SMALL_CTAS, 1, 1) __launch_bounds__(PLAN_T)
+    k_pages_reserve_small(Book bk, const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ new_tokens,
+                          int32_t* lacking, ReservePlan ws, const __grid_constant__ CopyArgs<N> a) {
+  if (blockIdx.x == 0) reserve_plan(bk, seq_lens, new_tokens, lacking, ws, a.list.status);
+  __syncwarp();
+  pair::cluster_sync();  // the plan is visible to the cluster
+  copy_tiles<PLAN_T>(a.list, a.seg, blockIdx.x, SMALL_CTAS);
 }
 
 // ---------------------------------------------------------------- host side
@@ -465,33 +504,53 @@ Book book_of(const gemma_page_book* b) {
   return Book{b->page_table, b->ref_count, b->n_seqs, b->pages_per_seq, b->n_pages, b->page_size};
 }
 
-// Copies the listed pages of every pool; a.src .. a.status are filled in.
-// max_pairs bounds the pairs (sizes the grid).
-cudaError_t copy_pages(CopyArgs& a, const gemma_page_pool* pools, int n_pools, int64_t max_pairs, cudaStream_t st) {
-  for (int i0 = 0; i0 < n_pools; i0 += MAX_SEGS / 2) {
-    a.n_segs = a.tiles = 0;
-    for (int i = i0; i < std::min(n_pools, i0 + MAX_SEGS / 2); ++i) {
-      const gemma_page_pool& p = pools[i];
-      const bool q8 = p.flags & GEMMA_F_KV_INT8;
-      for (int part = 0; part < (q8 ? 2 : 1); ++part) {
-        Seg g{};
-        const int row = part ? 8 : p.head_dim * (q8 ? 1 : 2);
-        g.base = static_cast<unsigned char*>(p.pool) +
-                 (part ? gemma_kv_codes_bytes(a.n_pages, p.n_kv_heads, a.ps, p.head_dim) : 0);
-        g.page_bytes = (long long)p.n_kv_heads * a.ps * row;
-        // whole pages are one run; partial ones a run per head
-        g.heads = a.rows ? p.n_kv_heads : 1;
-        g.row_bytes = a.rows ? row : row * p.n_kv_heads;
-        g.head_bytes = a.ps * g.row_bytes;
-        g.tiles_per_head = (g.head_bytes + TILE_B - 1) / TILE_B;
-        g.tile0 = a.tiles;
-        a.tiles += g.heads * g.tiles_per_head;
-        a.seg[a.n_segs++] = g;
-      }
+// Segments of pools [i0, i0 + MAX_SEGS / 2) and their tiles.
+void segments(CopyList& a, Seg* seg, const gemma_page_pool* pools, int n_pools, int i0) {
+  a.n_segs = a.tiles = 0;
+  for (int i = i0; i < std::min(n_pools, i0 + MAX_SEGS / 2); ++i) {
+    const gemma_page_pool& p = pools[i];
+    const bool q8 = p.flags & GEMMA_F_KV_INT8;
+    for (int part = 0; part < (q8 ? 2 : 1); ++part) {
+      Seg g{};
+      const int row = part ? 8 : p.head_dim * (q8 ? 1 : 2);
+      g.base = static_cast<unsigned char*>(p.pool) +
+               (part ? gemma_kv_codes_bytes(a.n_pages, p.n_kv_heads, a.ps, p.head_dim) : 0);
+      g.page_bytes = (long long)p.n_kv_heads * a.ps * row;
+      // whole pages are one run; partial ones a run per head
+      const int heads = a.rows ? p.n_kv_heads : 1;
+      g.row_bytes = a.rows ? row : row * p.n_kv_heads;
+      g.head_bytes = a.ps * g.row_bytes;
+      g.tiles_per_head = (g.head_bytes + TILE_B - 1) / TILE_B;
+      g.tile0 = a.tiles;
+      a.tiles += heads * g.tiles_per_head;
+      seg[a.n_segs++] = g;
     }
-    const int64_t grid = std::min<int64_t>(max_pairs * a.tiles, (int64_t)multiprocessors() * 8);
-    k_pages_copy<<<(unsigned)std::max<int64_t>(grid, 1), COPY_T, 0, st>>>(a);
-    const cudaError_t e = cudaGetLastError();
+  }
+}
+
+template <int N>
+cudaError_t launch_copy(const CopyList& list, const Seg* seg, int64_t work, const Book& bk, const int32_t* map,
+                        cudaStream_t st) {
+  CopyArgs<N> a;
+  a.list = list;
+  std::copy(seg, seg + list.n_segs, a.seg);
+  const int64_t grid = std::min<int64_t>(work, (int64_t)multiprocessors() * 8);
+  k_pages_copy<N><<<(unsigned)std::max<int64_t>(grid, 1), COPY_T, 0, st>>>(a, bk, map);
+  return cudaGetLastError();
+}
+
+// Copies the listed pages of every pool (max_pairs bounds the pairs), and
+// renames the book's entries by `map` if given.
+cudaError_t copy_pages(CopyList& list, const gemma_page_pool* pools, int n_pools, int64_t max_pairs, const Book& bk,
+                       const int32_t* map, cudaStream_t st) {
+  Seg seg[MAX_SEGS];
+  for (int i0 = 0; i0 == 0 || i0 < n_pools; i0 += MAX_SEGS / 2) {
+    segments(list, seg, pools, n_pools, i0);
+    if (i0) map = nullptr;
+    const int64_t names = map ? ((int64_t)bk.n_seqs * bk.pps + COPY_T - 1) / COPY_T : 0;
+    const int64_t work = std::max(max_pairs * list.tiles, names);
+    const cudaError_t e = list.n_segs <= FEW_SEGS ? launch_copy<FEW_SEGS>(list, seg, work, bk, map, st)
+                                                  : launch_copy<MAX_SEGS>(list, seg, work, bk, map, st);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -532,7 +591,8 @@ int gemma_kv_pages_fork(const gemma_page_book* book, const int32_t* parents, voi
   int* status = device_status();
   if (!status) return err(GEMMA_ERR_CUDA, "no CUDA device");
   const int smem = book->n_seqs * FORK_C * 4;
-  cudaError_t e = cudaFuncSetAttribute(k_pages_fork, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SEQS * FORK_C * 4);
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024) e = cudaFuncSetAttribute(k_pages_fork, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_err(e, "page fork");
   k_pages_fork<<<(book->pages_per_seq + FORK_C - 1) / FORK_C, 256, smem, static_cast<cudaStream_t>(stream)>>>(
       book_of(book), parents, status);
@@ -581,22 +641,33 @@ int gemma_kv_pages_reserve(const gemma_page_book* book, const gemma_page_pool* p
   plan.fresh = take(n_pages);
   plan.slots = take(slots);
   plan.copies = take(3 * (int64_t)book->n_seqs);
+  CopyList a{};
+  a.src = plan.copies;
+  a.dst = plan.copies + 1;
+  a.rows = plan.copies + 2;
+  a.stride = 3;
+  a.n_dev = plan.n_copies;
+  a.n_pages = book->n_pages;
+  a.ps = book->page_size;
+  a.status = status;
+  // One cluster copies about 0.4 MB a us, the whole GPU 3 MB, but in a second
+  // launch: up to 4 MB of tails (all rows splitting full pages) the cluster.
+  double most = 0.0;
+  for (int i = 0; i < n_pools; ++i)
+    most += (double)book->n_seqs * pools[i].n_kv_heads * book->page_size * pools[i].head_dim * 2;
+  if (n_pools > 0 && n_pools <= FEW_SEGS / 2 && most <= 4e6) {
+    CopyArgs<FEW_SEGS> c;
+    segments(a, c.seg, pools, n_pools, 0);
+    c.list = a;
+    k_pages_reserve_small<FEW_SEGS><<<SMALL_CTAS, PLAN_T, 0, st>>>(book_of(book), seq_lens, new_tokens, lacking, plan, c);
+    const cudaError_t es = cudaGetLastError();
+    return es != cudaSuccess ? cuda_err(es, "page reserve launch") : record_ok();
+  }
   k_pages_reserve<<<1, PLAN_T, 0, st>>>(book_of(book), seq_lens, new_tokens, lacking, plan, status);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_err(e, "page reserve launch");
   if (n_pools > 0) {
-    CopyArgs a;
-    a.src = plan.copies;
-    a.dst = plan.copies + 1;
-    a.rows = plan.copies + 2;
-    a.stride = 3;
-    a.n_dev = plan.n_copies;
-    a.n_host = 0;
-    a.n_pages = book->n_pages;
-    a.ps = book->page_size;
-    a.check = 0;
-    a.status = status;
-    e = copy_pages(a, pools, n_pools, book->n_seqs, st);
+    e = copy_pages(a, pools, n_pools, book->n_seqs, book_of(book), nullptr, st);
     if (e != cudaSuccess) return cuda_err(e, "page copy launch");
   }
   return record_ok();
@@ -628,33 +699,23 @@ int gemma_kv_pages_compact(const gemma_page_book* book, const gemma_page_pool* p
   plan.movers = take(n_pages);
   plan.copies = take(3 * n_pages);
   if (page_map) plan.map = page_map;
-  const int max_smem = (MAX_PAGES / 32) * 4;
-  cudaError_t e = cudaFuncSetAttribute(k_pages_compact, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
+  const int smem = (book->n_pages + 31) / 32 * 4;
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024) e = cudaFuncSetAttribute(k_pages_compact, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_err(e, "page compact");
-  k_pages_compact<<<1, PLAN_T, (book->n_pages + 31) / 32 * 4, st>>>(book_of(book), plan, n_live);
+  k_pages_compact<<<1, PLAN_T, smem, st>>>(book_of(book), plan, n_live);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_err(e, "page compact launch");
-  const int64_t entries = (int64_t)book->n_seqs * book->pages_per_seq;
-  const unsigned grid = (unsigned)std::min<int64_t>((entries + 255) / 256, (int64_t)multiprocessors() * 8);
-  k_pages_rename<<<grid, 256, 0, st>>>(book_of(book), plan.map, status);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_err(e, "page rename launch");
-  if (n_pools > 0) {
-    CopyArgs a;
-    a.src = plan.copies;
-    a.dst = plan.copies + 1;
-    a.rows = nullptr;
-    a.stride = 3;
-    a.n_dev = plan.n_copies;
-    a.n_host = 0;
-    a.n_pages = book->n_pages;
-    a.ps = book->page_size;
-    a.check = 0;
-    a.status = status;
-    e = copy_pages(a, pools, n_pools, std::max(1, book->n_pages / 2), st);
-    if (e != cudaSuccess) return cuda_err(e, "page copy launch");
-  }
-  return record_ok();
+  CopyList a{};
+  a.src = plan.copies;
+  a.dst = plan.copies + 1;
+  a.stride = 3;
+  a.n_dev = plan.n_copies;
+  a.n_pages = book->n_pages;
+  a.ps = book->page_size;
+  a.status = status;
+  e = copy_pages(a, pools, n_pools, std::max(1, book->n_pages / 2), book_of(book), plan.map, st);
+  return e != cudaSuccess ? cuda_err(e, "page copy launch") : record_ok();
 }
 
 int gemma_kv_pages_copy(const gemma_page_pool* pools, int n_pools, int n_pages, int page_size, const int32_t* src,
@@ -670,18 +731,17 @@ int gemma_kv_pages_copy(const gemma_page_pool* pools, int n_pools, int n_pages, 
     return err(GEMMA_ERR_INVALID_ARG, "src, dst: null or misaligned pointer");
   int* status = device_status();
   if (!status) return err(GEMMA_ERR_CUDA, "no CUDA device");
-  CopyArgs a;
+  CopyList a{};
   a.src = src;
   a.dst = dst;
-  a.rows = nullptr;
   a.stride = 1;
-  a.n_dev = nullptr;
   a.n_host = n_copies;
   a.n_pages = n_pages;
   a.ps = page_size;
   a.check = 1;
   a.status = status;
-  const cudaError_t e = copy_pages(a, pools, n_pools, n_copies, static_cast<cudaStream_t>(stream));
+  const cudaError_t e =
+      copy_pages(a, pools, n_pools, n_copies, Book{}, nullptr, static_cast<cudaStream_t>(stream));
   return e != cudaSuccess ? cuda_err(e, "page copy launch") : record_ok();
 }
 

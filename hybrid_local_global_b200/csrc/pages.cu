@@ -534,7 +534,8 @@ cudaError_t launch_copy(const CopyList& list, const Seg* seg, int64_t work, cons
   CopyArgs<N> a;
   a.list = list;
   std::copy(seg, seg + list.n_segs, a.seg);
-  const int64_t grid = std::min<int64_t>(work, (int64_t)multiprocessors() * 8);
+  // 32 CTAs per SM in all (256 MB: 42 us, 92 % of the copy rate; 8 per SM: 45)
+  const int64_t grid = std::min<int64_t>(work, (int64_t)multiprocessors() * 32);
   k_pages_copy<N><<<(unsigned)std::max<int64_t>(grid, 1), COPY_T, 0, st>>>(a, bk, map);
   return cudaGetLastError();
 }

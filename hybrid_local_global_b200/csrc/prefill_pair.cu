@@ -22,7 +22,7 @@
 //              output columns (one stage).
 //              Both CTAs' loads of a stage complete on the leader's barrier
 //              (cta_group::2 loads, no multicast), which expects both halves.
-//   warp 1     TMEM owner (both CTAs); in the leader, one lane issues the
+//   warp 1     TMEM owner (both CTAs); in the leader, the warp issues the
 //              MMAs: S_j = Q K_j^T (M=256, N=128, K=D) into one of two
 //              128-column TMEM buffers, then O += P_{j-1} V_{j-1} (M=256,
 //              N=256, K=128) with P read from both CTAs' TMEM; commits arrive
@@ -34,7 +34,7 @@
 // each; the fp32 O tile of 128 x 512 would fill TMEM), each computing S.
 //
 // V rows past the sequence end must be finite (their P is 0, but 0 * inf is
-// nan): on the one key tile that crosses the end, the MMA lane clears those
+// nan): on the one key tile that crosses the end, the MMA warp clears those
 // rows in both CTAs' stages before the P.V product.
 //
 // Every wait is bounded by a %globaltimer deadline. On a timeout the CTA
@@ -158,19 +158,17 @@ __device__ __forceinline__ float max_row(const uint32_t (&r)[4][32]) {
   return max8(mx);
 }
 
-// Zero V rows [r0, BN) of a stage: both 64-column boxes, in this CTA (local
+// Zero V rows [r0, BN) of a stage (the whole warp): both 64-column boxes, in this CTA (local
 // stores) and in the peer (distributed shared memory), then make the writes
 // visible to the tensor core's reads.
-__device__ __forceinline__ void clear_v_tail_pair(uint32_t stage, int r0) {
+__device__ __forceinline__ void clear_v_tail_pair(uint32_t stage, int r0, int lane) {
   const uint32_t peer = pair::map_to(stage, 1);
   const uint32_t self = pair::map_to(stage, 0);
-  for (int r = r0; r < BN; ++r)
-    for (int c = 0; c < 2; ++c)
-      for (int u = 0; u < 8; ++u) {
-        const uint32_t off = (uint32_t)(c * CHUNK_V + r * 128 + u * 16);
-        asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(self + off), "r"(0) : "memory");
-        asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(peer + off), "r"(0) : "memory");
-      }
+  for (int i = lane; i < (BN - r0) * 16; i += 32) {
+    const uint32_t off = (uint32_t)(((i >> 3) & 1) * CHUNK_V + (r0 + (i >> 4)) * 128 + (i & 7) * 16);
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(self + off), "r"(0) : "memory");
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(peer + off), "r"(0) : "memory");
+  }
   asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
 }
 
@@ -257,63 +255,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
-    if (lane == 0) {
+    const uint32_t go = tc::elect_one();
+    // both CTAs' halves complete on the leader's barriers, which expect both
+    const uint32_t q_bar = pair::map_to(smem_u32(&ctl->q_full), 0);
+    if (go) {
       tc::prefetch_tmap(&tm_q);
       tc::prefetch_tmap(&tm_k);
       tc::prefetch_tmap(&tm_v);
-      // both CTAs' halves complete on the leader's barriers, which expect both
-      const uint32_t q_bar = pair::map_to(smem_u32(&ctl->q_full), 0);
       if (leader) mbar_arrive_expect_tx(&ctl->q_full, 2 * Q_B);
-      for (int c = 0; c < D / 64; ++c) pair::tma_load_4d_pair(sQ + c * CHUNK_Q, &tm_q, c * 64, h, q0, b, q_bar);
       ctl->q_issued = 1;
-      int item = 0;
-      bool ok = true;
-      for (int j = 0; j <= n_tiles && ok; ++j) {
-        for (int kind = 0; kind < 2 && ok; ++kind) {  // 0: K_j, 1: V_{j-1}
-          if ((kind == 0 && j == n_tiles) || (kind == 1 && j == 0)) continue;
-          int key0 = (int)(tile_key(j - kind) - koff);  // view row
-          int kb = b;                                           // view batch
-          if (a.page_table) {
-            // tiles never straddle a page (page_size is a multiple of 128); a
-            // tile past the sequence's pages holds no visible key: any page
-            const int pi = key0 / a.page_size;
-            kb = pi < a.pages_per_seq ? a.page_table[(int64_t)b * a.pages_per_seq + pi] : 0;
-            if (kb < 0 || kb >= a.n_pages) {
-              if ((int64_t)key0 < n_keys) set_status(a.status, GEMMA_ERR_DEVICE_RANGE);
-              kb = 0;
-            }
-            key0 -= pi * a.page_size;
+    }
+    __syncwarp();
+    for (int c = 0; c < D / 64; ++c) pair::tma_load_4d_pair_if(go, sQ + c * CHUNK_Q, &tm_q, c * 64, h, q0, b, q_bar);
+    int item = 0;
+    bool ok = true;
+    for (int j = 0; j <= n_tiles && ok; ++j) {
+      for (int kind = 0; kind < 2 && ok; ++kind) {  // 0: K_j, 1: V_{j-1}
+        if ((kind == 0 && j == n_tiles) || (kind == 1 && j == 0)) continue;
+        int key0 = (int)(tile_key(j - kind) - koff);  // view row
+        int kb = b;                                   // view batch
+        if (a.page_table) {
+          // tiles never straddle a page (page_size is a multiple of 128); a
+          // tile past the sequence's pages holds no visible key: any page
+          const int pi = key0 / a.page_size;
+          kb = pi < a.pages_per_seq ? a.page_table[(int64_t)b * a.pages_per_seq + pi] : 0;
+          if (kb < 0 || kb >= a.n_pages) {
+            if (go && (int64_t)key0 < n_keys) set_status(a.status, GEMMA_ERR_DEVICE_RANGE);
+            kb = 0;
           }
-          const int n_stg = kind == 0 ? Cfg::K_STAGES : 1;
-          for (int hs = 0; hs < n_stg; ++hs, ++item) {
-            const int s = item % NSTAGE;
-            if (item >= NSTAGE &&
-                !mbar_wait_bounded_at(&ctl->empty[s], ((item / NSTAGE) - 1) & 1, abort_flag, deadline,
-                                      a.status, 31, item, s, j)) {
-              ok = false;
-              break;
-            }
-            const uint32_t dst = sStage + s * STAGE_B;
-            const uint32_t bar = pair::map_to(smem_u32(&ctl->full[s]), 0);
+          key0 -= pi * a.page_size;
+        }
+        const int n_stg = kind == 0 ? Cfg::K_STAGES : 1;
+        for (int hs = 0; hs < n_stg; ++hs, ++item) {
+          const int s = item % NSTAGE;
+          if (item >= NSTAGE &&
+              !wait_all(&ctl->empty[s], ((item / NSTAGE) - 1) & 1, abort_flag, deadline, a.status, 31, item, s, j)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = sStage + s * STAGE_B;
+          const uint32_t bar = pair::map_to(smem_u32(&ctl->full[s]), 0);
+          if (go) {
             if (leader) mbar_arrive_expect_tx(&ctl->full[s], 2 * STAGE_B);
             ctl->issued[s] += 1;
-            if (kind == 0) {
-              const int k0 = key0 + (int)rank * KH;  // this CTA's 64 keys
-              for (int cc = 0; cc < 4; ++cc) {
-                const int d0 = (hs * 4 + cc) * 64;
-                if (a.kv_token_major)
-                  pair::tma_load_4d_pair(dst + cc * CHUNK_K, &tm_k, d0, g, k0, kb, bar);
-                else
-                  pair::tma_load_4d_pair(dst + cc * CHUNK_K, &tm_k, d0, k0, g, kb, bar);
-              }
-            } else {
-              const int c0 = vh * DV + (int)rank * VH;  // this CTA's 128 output columns
-              for (int c = 0; c < 2; ++c) {
-                if (a.kv_token_major)
-                  pair::tma_load_4d_pair(dst + c * CHUNK_V, &tm_v, c0 + c * 64, g, key0, kb, bar);
-                else
-                  pair::tma_load_4d_pair(dst + c * CHUNK_V, &tm_v, c0 + c * 64, key0, g, kb, bar);
-              }
+          }
+          __syncwarp();
+          if (kind == 0) {
+            const int k0 = key0 + (int)rank * KH;  // this CTA's 64 keys
+            for (int cc = 0; cc < 4; ++cc) {
+              const int d0 = (hs * 4 + cc) * 64;
+              if (a.kv_token_major)
+                pair::tma_load_4d_pair_if(go, dst + cc * CHUNK_K, &tm_k, d0, g, k0, kb, bar);
+              else
+                pair::tma_load_4d_pair_if(go, dst + cc * CHUNK_K, &tm_k, d0, k0, g, kb, bar);
+            }
+          } else {
+            const int c0 = vh * DV + (int)rank * VH;  // this CTA's 128 output columns
+            for (int c = 0; c < 2; ++c) {
+              if (a.kv_token_major)
+                pair::tma_load_4d_pair_if(go, dst + c * CHUNK_V, &tm_v, c0 + c * 64, g, key0, kb, bar);
+              else
+                pair::tma_load_4d_pair_if(go, dst + c * CHUNK_V, &tm_v, c0 + c * 64, key0, g, kb, bar);
             }
           }
         }
@@ -321,67 +323,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (leader, one lane)
-    if (leader && lane == 0) {
-      bool ok = mbar_wait_bounded_at(&ctl->q_full, 0, abort_flag, deadline, a.status, 30, 0, 0, 0);
-      if (ok) ctl->q_consumed = 1;
-      int item = 0;
+    // ------------------------------------------------------------ MMA issuer (leader)
+    if (leader) {
+      const uint32_t go = tc::elect_one();
+      bool ok = wait_all(&ctl->q_full, 0, abort_flag, deadline, a.status, 30);
+      if (ok && go) ctl->q_consumed = 1;
+      const uint64_t dq = tc::smem_desc_sw128(sQ, 16, 1024);
+      const uint64_t dk = tc::smem_desc_sw128(sStage, 16, 1024), dv = tc::smem_desc_sw128(sStage, CHUNK_V, 1024);
+      int item = 0, taken = 0;
       for (int j = 0; j <= n_tiles && ok; ++j) {
         if (j < n_tiles) {
           const uint32_t d_s = tmem + COL_S + (uint32_t)(j & 1) * 128;
           for (int hs = 0; hs < Cfg::K_STAGES; ++hs, ++item) {
             const int s = item % NSTAGE;
-            if (!mbar_wait_bounded_at(&ctl->full[s], (item / NSTAGE) & 1, abort_flag, deadline, a.status, 32,
-                                      item, s, j)) {
+            if (!wait_all(&ctl->full[s], (item / NSTAGE) & 1, abort_flag, deadline, a.status, 32, item, s, j)) {
               ok = false;
               break;
             }
-            ctl->consumed[s] += 1;
+            taken = item + 1;
             tc::fence_after_sync();
-            const uint32_t st = sStage + s * STAGE_B;
 #pragma unroll
             for (int cc = 0; cc < 4; ++cc)
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                const uint64_t da = tc::smem_desc_sw128(sQ + (hs * 4 + cc) * CHUNK_Q + kk * 32, 16, 1024);
-                const uint64_t db = tc::smem_desc_sw128(st + cc * CHUNK_K + kk * 32, 16, 1024);
-                pair::mma2_ss(d_s, da, db, IDESC_S, (hs | cc | kk) != 0);
-              }
-            pair::commit2_mc(smem_u32(&ctl->empty[s]), BOTH);
+              for (int kk = 0; kk < 4; ++kk)
+                pair::mma2_ss_if(go, d_s, dq + (uint64_t)(((hs * 4 + cc) * CHUNK_Q + kk * 32) >> 4),
+                                 dk + (uint64_t)((s * STAGE_B + cc * CHUNK_K + kk * 32) >> 4), IDESC_S,
+                                 (hs | cc | kk) != 0);
+            pair::commit2_mc_if(go, smem_u32(&ctl->empty[s]), BOTH);
           }
           if (!ok) break;
-          pair::commit2_mc(smem_u32(&ctl->s_full[j & 1]), BOTH);
+          pair::commit2_mc_if(go, smem_u32(&ctl->s_full[j & 1]), BOTH);
         }
         if (j >= 1) {
-          if (!pair::wait_bounded_cluster(&ctl->p_ready, (j - 1) & 1, abort_flag, deadline, a.status, 34, j, 0,
-                                          0)) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xffffffffu, pair::wait_bounded_cluster(&ctl->p_ready, (j - 1) & 1, abort_flag, deadline,
+                                                                  a.status, 34, j, 0, 0));
+          if (!ok) break;
           const uint32_t p_tm = tmem + COL_S + (uint32_t)((j - 1) & 1) * 128;
           const int s = item % NSTAGE;
-          if (!mbar_wait_bounded_at(&ctl->full[s], (item / NSTAGE) & 1, abort_flag, deadline, a.status, 35,
-                                    item, s, j)) {
+          if (!wait_all(&ctl->full[s], (item / NSTAGE) & 1, abort_flag, deadline, a.status, 35, item, s, j)) {
             ok = false;
             break;
           }
-          ctl->consumed[s] += 1;
-          const uint32_t st = sStage + s * STAGE_B;
+          taken = item + 1;
           const int64_t rows_valid = n_keys - tile_key(j - 1);
-          if (rows_valid < BN) clear_v_tail_pair(st, rows_valid > 0 ? (int)rows_valid : 0);
+          if (rows_valid < BN) {
+            clear_v_tail_pair(sStage + s * STAGE_B, rows_valid > 0 ? (int)rows_valid : 0, lane);
+            __syncwarp();
+          }
           tc::fence_after_sync();
 #pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk) {
-            const uint64_t db = tc::smem_desc_sw128(st + kk * 2048, CHUNK_V, 1024);
-            pair::mma2_ts(tmem + COL_O, p_tm + kk * 8, db, IDESC_PV, (j - 1 > 0 || kk) ? 1u : 0u);
-          }
-          pair::commit2_mc(smem_u32(&ctl->empty[s]), BOTH);
-          pair::commit2_mc(smem_u32(&ctl->o_done[(j - 1) & 1]), BOTH);
+          for (int kk = 0; kk < BN / 16; ++kk)
+            pair::mma2_ts_if(go, tmem + COL_O, p_tm + kk * 8, dv + (uint64_t)((s * STAGE_B + kk * 2048) >> 4), IDESC_PV,
+                             (j - 1 > 0 || kk) ? 1u : 0u);
+          pair::commit2_mc_if(go, smem_u32(&ctl->empty[s]), BOTH);
+          pair::commit2_mc_if(go, smem_u32(&ctl->o_done[(j - 1) & 1]), BOTH);
           ++item;
         }
       }
       // no MMA may be in flight when either CTA releases TMEM or shared memory
-      pair::commit2_mc(smem_u32(&ctl->drain), BOTH);
+      pair::commit2_mc_if(go, smem_u32(&ctl->drain), BOTH);
+      if (go)
+        for (int s = 0; s < NSTAGE; ++s) ctl->consumed[s] = (taken + NSTAGE - 1 - s) / NSTAGE;
     }
     __syncwarp();
     // the leader's MMAs read both CTAs' shared memory and write both TMEMs

@@ -15,7 +15,7 @@
 //              a ring of 32 KB stages in MMA order: K_0, K_1, V_0, K_2, V_1,
 //              ... (a K tile = D/128 stages of 128 keys x 128 dims, a V tile
 //              = 2 stages of 64 keys x 256 dims; 128-byte swizzle).
-//   warp 1     TMEM owner and MMA issuer (one lane): S_j = Q K_j^T into one
+//   warp 1     TMEM owner and MMA issuer: S_j = Q K_j^T into one
 //              of two 128-column TMEM buffers (M=128, N=128, K=D), then
 //              O += P_{j-1} V_{j-1} (M=128, N=256, K=128) with P read from
 //              TMEM; tcgen05.commit frees smem stages and signals S / O.
@@ -252,68 +252,70 @@ __global__ void __launch_bounds__(192, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
+    const uint32_t go = tc::elect_one();
+    if (go) {
       tc::prefetch_tmap(&tm_q);
       tc::prefetch_tmap(&tm_k);
       tc::prefetch_tmap(&tm_v);
-      if (VF) {
-        // G heads x tokens rows; the tile's other rows are never stored
-        mbar_arrive_expect_tx(&ctl->q_full, (uint32_t)(D * 2 * G * a.tokens));
-        for (int c = 0; c < D / 64; ++c)
-          tc::tma_load_4d(sQ + c * CHUNK_B, &tm_q, c * 64, g * G, 0, b, smem_u32(&ctl->q_full));
-      } else {
-        mbar_arrive_expect_tx(&ctl->q_full, Q_B);
-        for (int c = 0; c < D / 64; ++c)
-          tc::tma_load_4d(sQ + c * CHUNK_B, &tm_q, c * 64, h, q0, b, smem_u32(&ctl->q_full));
-      }
+      // VF: G heads x tokens rows; the tile's other rows are never stored
+      mbar_arrive_expect_tx(&ctl->q_full, VF ? (uint32_t)(D * 2 * G * a.tokens) : (uint32_t)Q_B);
       ctl->q_issued = 1;
-      int item = 0;
-      bool ok = true;
-      for (int j = 0; j <= n_tiles && ok; ++j) {
-        for (int kind = 0; kind < 2 && ok; ++kind) {  // 0: K_j, 1: V_{j-1}
-          if ((kind == 0 && j == n_tiles) || (kind == 1 && j == 0)) continue;
-          int key0 = (int)(tile_key(j - kind) - koff);  // view row
-          int kb = b;                                           // view batch
-          if (a.page_table) {
-            // tiles never straddle a page (page_size is a multiple of 128); a
-            // tile past the sequence's pages holds no visible key: any page
-            const int pi = key0 / a.page_size;
-            kb = pi < a.pages_per_seq ? a.page_table[(int64_t)b * a.pages_per_seq + pi] : 0;
-            if (kb < 0 || kb >= a.n_pages) {
-              if ((int64_t)key0 < n_keys) set_status(a.status, GEMMA_ERR_DEVICE_RANGE);
-              kb = 0;
-            }
-            key0 -= pi * a.page_size;
+    }
+    __syncwarp();
+    for (int c = 0; c < D / 64; ++c) {
+      if (VF)
+        tc::tma_load_4d_if(go, sQ + c * CHUNK_B, &tm_q, c * 64, g * G, 0, b, smem_u32(&ctl->q_full));
+      else
+        tc::tma_load_4d_if(go, sQ + c * CHUNK_B, &tm_q, c * 64, h, q0, b, smem_u32(&ctl->q_full));
+    }
+    int item = 0;
+    bool ok = true;
+    for (int j = 0; j <= n_tiles && ok; ++j) {
+      for (int kind = 0; kind < 2 && ok; ++kind) {  // 0: K_j, 1: V_{j-1}
+        if ((kind == 0 && j == n_tiles) || (kind == 1 && j == 0)) continue;
+        int key0 = (int)(tile_key(j - kind) - koff);  // view row
+        int kb = b;                                   // view batch
+        if (a.page_table) {
+          // tiles never straddle a page (page_size is a multiple of 128); a
+          // tile past the sequence's pages holds no visible key: any page
+          const int pi = key0 / a.page_size;
+          kb = pi < a.pages_per_seq ? a.page_table[(int64_t)b * a.pages_per_seq + pi] : 0;
+          if (kb < 0 || kb >= a.n_pages) {
+            if (go && (int64_t)key0 < n_keys) set_status(a.status, GEMMA_ERR_DEVICE_RANGE);
+            kb = 0;
           }
-          const int n_stg = kind == 0 ? Cfg::K_STAGES : 2;
-          for (int half = 0; half < n_stg; ++half, ++item) {
-            const int s = item % NSTAGE;
-            if (item >= NSTAGE &&
-                !mbar_wait_bounded_at(&ctl->empty[s], ((item / NSTAGE) - 1) & 1, abort_flag, deadline,
-                                      a.status, 11, item, s, j)) {
-              ok = false;
-              break;
-            }
-            const uint32_t dst = sStage + s * STAGE_B;
-            const uint32_t bar = smem_u32(&ctl->full[s]);
+          key0 -= pi * a.page_size;
+        }
+        const int n_stg = kind == 0 ? Cfg::K_STAGES : 2;
+        for (int half = 0; half < n_stg; ++half, ++item) {
+          const int s = item % NSTAGE;
+          if (item >= NSTAGE &&
+              !wait_all(&ctl->empty[s], ((item / NSTAGE) - 1) & 1, abort_flag, deadline, a.status, 11, item, s, j)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = sStage + s * STAGE_B;
+          const uint32_t bar = smem_u32(&ctl->full[s]);
+          if (go) {
             mbar_arrive_expect_tx(&ctl->full[s], STAGE_B);
             ctl->issued[s] += 1;
-            if (kind == 0) {
-              for (int cc = 0; cc < 2; ++cc) {
-                const int d0 = (half * 2 + cc) * 64;
-                if (a.kv_token_major)
-                  tc::tma_load_4d(dst + cc * CHUNK_B, &tm_k, d0, g, key0, kb, bar);
-                else
-                  tc::tma_load_4d(dst + cc * CHUNK_B, &tm_k, d0, key0, g, kb, bar);
-              }
-            } else {
-              const int k0 = key0 + half * 64;
-              for (int c = 0; c < 4; ++c) {
-                if (a.kv_token_major)
-                  tc::tma_load_4d(dst + c * 8192, &tm_v, vh * DV + c * 64, g, k0, kb, bar);
-                else
-                  tc::tma_load_4d(dst + c * 8192, &tm_v, vh * DV + c * 64, k0, g, kb, bar);
-              }
+          }
+          __syncwarp();
+          if (kind == 0) {
+            for (int cc = 0; cc < 2; ++cc) {
+              const int d0 = (half * 2 + cc) * 64;
+              if (a.kv_token_major)
+                tc::tma_load_4d_if(go, dst + cc * CHUNK_B, &tm_k, d0, g, key0, kb, bar);
+              else
+                tc::tma_load_4d_if(go, dst + cc * CHUNK_B, &tm_k, d0, key0, g, kb, bar);
+            }
+          } else {
+            const int k0 = key0 + half * 64;
+            for (int c = 0; c < 4; ++c) {
+              if (a.kv_token_major)
+                tc::tma_load_4d_if(go, dst + c * 8192, &tm_v, vh * DV + c * 64, g, k0, kb, bar);
+              else
+                tc::tma_load_4d_if(go, dst + c * 8192, &tm_v, vh * DV + c * 64, k0, g, kb, bar);
             }
           }
         }
@@ -322,9 +324,12 @@ __global__ void __launch_bounds__(192, 1)
     __syncwarp();  // reconverge before the block barrier below
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
+    const uint32_t go = tc::elect_one();
     bool ok = wait_all(&ctl->q_full, 0, abort_flag, deadline, a.status, 10);
-    if (ok && lane == 0) ctl->q_consumed = 1;
-    int item = 0;
+    if (ok && go) ctl->q_consumed = 1;
+    const uint64_t dq = tc::smem_desc_sw128(sQ, 16, 1024);
+    const uint64_t dk = tc::smem_desc_sw128(sStage, 16, 1024), dv = tc::smem_desc_sw128(sStage, 8192, 1024);
+    int item = 0, taken = 0;
     for (int j = 0; j <= n_tiles && ok; ++j) {
       if (j < n_tiles) {
         const uint32_t d_s = tmem + COL_S + (uint32_t)(j & 1) * 128;
@@ -334,24 +339,19 @@ __global__ void __launch_bounds__(192, 1)
             ok = false;
             break;
           }
-          if (lane == 0) {
-            ctl->consumed[s] += 1;
-            tc::fence_after_sync();
-            const uint32_t st = sStage + s * STAGE_B;
+          taken = item + 1;
+          tc::fence_after_sync();
 #pragma unroll
-            for (int cc = 0; cc < 2; ++cc)
+          for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                const uint64_t da = tc::smem_desc_sw128(sQ + (half * 2 + cc) * CHUNK_B + kk * 32, 16, 1024);
-                const uint64_t db = tc::smem_desc_sw128(st + cc * CHUNK_B + kk * 32, 16, 1024);
-                tc::mma_ss(d_s, da, db, IDESC_S, (half | cc | kk) != 0);
-              }
-            tc::commit(smem_u32(&ctl->empty[s]));
-          }
-          __syncwarp();
+            for (int kk = 0; kk < 4; ++kk)
+              tc::mma_ss_if(go, d_s, dq + (uint64_t)(((half * 2 + cc) * CHUNK_B + kk * 32) >> 4),
+                            dk + (uint64_t)((s * STAGE_B + cc * CHUNK_B + kk * 32) >> 4), IDESC_S,
+                            (half | cc | kk) != 0);
+          tc::commit_if(go, smem_u32(&ctl->empty[s]));
         }
         if (!ok) break;
-        if (lane == 0) tc::commit(smem_u32(&ctl->s_full[j & 1]));
+        tc::commit_if(go, smem_u32(&ctl->s_full[j & 1]));
       }
       if (j >= 1) {
         if (!wait_all(&ctl->p_ready, (j - 1) & 1, abort_flag, deadline, a.status, 13, j)) {
@@ -366,6 +366,7 @@ __global__ void __launch_bounds__(192, 1)
             ok = false;
             break;
           }
+          taken = item + 1;
           const uint32_t st = sStage + s * STAGE_B;
           const int64_t rows_valid = n_keys - (tile_key0 + half * 64);
           if (rows_valid < 64) {
@@ -379,26 +380,21 @@ __global__ void __launch_bounds__(192, 1)
             fence_proxy_async_smem();
             __syncwarp();
           }
-          if (lane == 0) {
-            ctl->consumed[s] += 1;
-            tc::fence_after_sync();
+          tc::fence_after_sync();
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t db = tc::smem_desc_sw128(st + kk * 2048, 8192, 1024);
-              tc::mma_ts(tmem + COL_O, p_tm + half * 32 + kk * 8, db, IDESC_PV,
-                         (j - 1 > 0 || half || kk) ? 1u : 0u);
-            }
-            tc::commit(smem_u32(&ctl->empty[s]));
-          }
-          __syncwarp();
+          for (int kk = 0; kk < 4; ++kk)
+            tc::mma_ts_if(go, tmem + COL_O, p_tm + half * 32 + kk * 8,
+                          dv + (uint64_t)((s * STAGE_B + kk * 2048) >> 4), IDESC_PV, (j - 1 > 0 || half || kk) ? 1u : 0u);
+          tc::commit_if(go, smem_u32(&ctl->empty[s]));
         }
         if (!ok) break;
-        if (lane == 0) tc::commit(smem_u32(&ctl->o_done[(j - 1) & 1]));
+        tc::commit_if(go, smem_u32(&ctl->o_done[(j - 1) & 1]));
       }
     }
     // make sure no MMA is in flight before TMEM can be released
-    if (lane == 0) {
-      tc::commit(smem_u32(&ctl->drain));
+    tc::commit_if(go, smem_u32(&ctl->drain));
+    if (go) {
+      for (int s = 0; s < NSTAGE; ++s) ctl->consumed[s] = (taken + NSTAGE - 1 - s) / NSTAGE;
       volatile int never = 0;
       mbar_wait_bounded_at(&ctl->drain, 0, &never, globaltimer_ns() + 200000000ull, a.status, 18, 0, 0, 0);
     }

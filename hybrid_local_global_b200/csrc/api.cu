@@ -1176,8 +1176,10 @@ int gemma_attn_prefill_sinks(const void* q, const void* k_new, const void* v_new
   const bool pair = head_dim == 512 && (n_q_heads / n_kv_heads) % 2 == 0;
   {
     ProfScope p_attn(GEMMA_KERNEL_PREFILL_ATTN, st);
-    e = pair ? launch_prefill_attn_pair(aa, batch, head_dim, page_size, 0, 1, st)
-             : launch_prefill_attn_tc(aa, batch, head_dim, page_size, 0, st);
+    const int splits = prefill_rows_splits(aa, batch, head_dim);
+    e = splits ? launch_prefill_attn_rows(aa, batch, head_dim, splits, st)
+        : pair ? launch_prefill_attn_pair(aa, batch, head_dim, page_size, 0, 1, st)
+               : launch_prefill_attn_tc(aa, batch, head_dim, page_size, 0, st);
     p_attn.done();
   }
   if (e != cudaSuccess) return cuda_fail(e, "prefill attention launch");

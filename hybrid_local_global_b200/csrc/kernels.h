@@ -223,6 +223,10 @@ cudaError_t launch_quantize_rows(const QuantRowsArgs& a, int B, int D, cudaStrea
 // sharing each MMA (cta_group::2).
 cudaError_t launch_prefill_attn_tc(const PrefillAttnArgs& a, int B, int D, int key_rows_total,
                                    int kv_token_major, cudaStream_t st);
+// Short chunks with window and sinks: the splits of the keys that
+// prefill_rows_splits gives (0: use the others) share the work of few rows.
+int prefill_rows_splits(const PrefillAttnArgs& a, int B, int D);
+cudaError_t launch_prefill_attn_rows(const PrefillAttnArgs& a, int B, int D, int n, cudaStream_t st);
 // head_pair: the pair takes two q heads of one KV head on the same query
 // tile (used when q heads per KV head is even) instead of two query tiles.
 cudaError_t launch_prefill_attn_pair(const PrefillAttnArgs& a, int B, int D, int key_rows_total,

@@ -39,8 +39,11 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
+#include "pair.cuh"
 #include "tc.cuh"
 #include "tmap.h"
 
@@ -161,6 +164,12 @@ __device__ __forceinline__ float max_row(const uint32_t (&r)[4][32]) {
 // the combine instead of bf16 rows.
 // SK: a window plus sinks (cache views): the key tiles of the sinks, then the
 // tiles from the window's first one on.
+// VF and SK: a short chunk with a window plus sinks. A CTA's rows are the G q
+// heads of one KV head for 128 / G tokens (as VF: the tile is full where a
+// chunk of one head would not fill it, and the heads share the keys), and the
+// CTAs of a cluster share the key tiles: few rows then still use many SMs. The
+// splits merge in distributed shared memory, each CTA for its share of the
+// columns, straight into the output.
 template <int D, bool VF, bool SK>
 __global__ void __launch_bounds__(192, 1)
     k_prefill_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -178,17 +187,21 @@ __global__ void __launch_bounds__(192, 1)
   Ctl<NSTAGE>* ctl = reinterpret_cast<Ctl<NSTAGE>*>(sm + Q_B + NSTAGE * STAGE_B);
   volatile int* abort_flag = &ctl->abort;
 
+  constexpr bool ROWS = VF && SK;
   const int G = a.Hq / a.Hkv;
-  const int vh = blockIdx.x % Cfg::NV, b = blockIdx.y;
+  const int unit = ROWS ? (int)blockIdx.y : (int)blockIdx.x;
+  const int vh = unit % Cfg::NV, b = ROWS ? blockIdx.z : blockIdx.y;
   const int h = VF ? 0 : (int)blockIdx.x / Cfg::NV;  // VF: per row, g * G + row % G
-  const int g = VF ? (int)blockIdx.x / Cfg::NV : h / G;
+  const int g = ROWS ? unit / Cfg::NV % a.Hkv : VF ? unit / Cfg::NV : h / G;
   const int q0 = VF ? 0 : (a.n_qtiles - 1 - (int)blockIdx.z) * BM;
+  const int t0 = ROWS ? unit / (Cfg::NV * a.Hkv) * a.tokens : 0;  // first token of the rows
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   int64_t pos0, n_keys, kt0;
   int n_tiles;
   int n_st = 0;  // SK: tiles of the sinks, before tile kt0
-  if (VF) {
+  int j0 = 0;    // ROWS: this CTA's first tile
+  if (VF && !SK) {
     // token t sits at position seq_lens[b] - tokens + t; this CTA reads keys
     // [split * chunk, min(+chunk, seq_lens[b]))
     n_keys = a.seq_lens[b];
@@ -204,11 +217,12 @@ __global__ void __launch_bounds__(192, 1)
   }
   // view row of a key = its position - koff (a gathered key window starts at pos0 - window)
   const int64_t koff = (!VF && a.key_off_window) ? pos0 - a.window : 0;
-  if (!VF) {
+  if (!VF || SK) {
     if (pos0 < 0 || n_keys - koff > a.key_cap) return;  // reported by the RoPE kernel
+    const int first = ROWS ? t0 : q0, last = min(ROWS ? t0 + a.tokens - 1 : q0 + BM - 1, a.S - 1);
     int64_t lo_first, hi_first, lo_last, hi_last;
-    visible_range(pos0 + q0, a.window, n_keys, &lo_first, &hi_first);
-    visible_range(pos0 + min(q0 + BM - 1, a.S - 1), a.window, n_keys, &lo_last, &hi_last);
+    visible_range(pos0 + first, a.window, n_keys, &lo_first, &hi_first);
+    visible_range(pos0 + last, a.window, n_keys, &lo_last, &hi_last);
     kt0 = lo_first / BN;
     n_tiles = (int)(hi_last / BN - kt0 + 1);
     if (SK) {
@@ -216,9 +230,17 @@ __global__ void __launch_bounds__(192, 1)
       n_st = (int)(sink_tiles < kt0 ? sink_tiles : kt0);
       n_tiles += n_st;
     }
+    if (ROWS) {
+      const int per = (n_tiles + (int)gridDim.x - 1) / (int)gridDim.x;
+      j0 = (int)blockIdx.x * per;
+      n_tiles = max(0, min(per, n_tiles - j0));
+    }
   }
   // first key of the j-th key tile
-  const auto tile_key = [&](int j) -> int64_t { return (SK && j < n_st ? j : kt0 + j - n_st) * BN; };
+  const auto tile_key = [&](int j) -> int64_t {
+    j += j0;
+    return (SK && j < n_st ? j : kt0 + j - n_st) * BN;
+  };
 
   if (threadIdx.x == 0) {
     mbar_init(&ctl->q_full, 1);
@@ -249,6 +271,7 @@ __global__ void __launch_bounds__(192, 1)
   tc::fence_after_sync();
   const uint32_t tmem = ctl->tmem_base;
   const uint64_t deadline = globaltimer_ns() + a.wait_ns;
+  float row_m = -INFINITY, row_l = 0.f;  // ROWS, softmax threads: the row's max and sum over this CTA's keys
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -264,7 +287,7 @@ __global__ void __launch_bounds__(192, 1)
     __syncwarp();
     for (int c = 0; c < D / 64; ++c) {
       if (VF)
-        tc::tma_load_4d_if(go, sQ + c * CHUNK_B, &tm_q, c * 64, g * G, 0, b, smem_u32(&ctl->q_full));
+        tc::tma_load_4d_if(go, sQ + c * CHUNK_B, &tm_q, c * 64, g * G, t0, b, smem_u32(&ctl->q_full));
       else
         tc::tma_load_4d_if(go, sQ + c * CHUNK_B, &tm_q, c * 64, h, q0, b, smem_u32(&ctl->q_full));
     }
@@ -404,9 +427,13 @@ __global__ void __launch_bounds__(192, 1)
     const int wq = warp & 3;
     const int row = wq * 32 + lane;
     const uint32_t tm = tmem + ((uint32_t)(wq * 32) << 16);
-    const bool row_valid = VF ? row < G * a.tokens : q0 + row < a.S;
+    const bool row_valid = VF ? row < G * a.tokens && t0 + row / G < a.S : q0 + row < a.S;
     int64_t lo, hi;
-    if (VF) {
+    if (ROWS) {
+      lo = 0;
+      hi = -1;  // a row past the tokens sees nothing
+      if (row_valid) visible_range(pos0 + t0 + row / G, a.window, n_keys, &lo, &hi);
+    } else if (VF) {
       // keys up to the row's token (global layer); a row past the tokens sees none
       lo = row_valid ? 0 : 1;
       hi = row_valid ? pos0 + row / G : 0;
@@ -510,16 +537,22 @@ __global__ void __launch_bounds__(192, 1)
       tc::fence_before_sync();
       mbar_arrive(&ctl->p_ready);
     }
-    if (ok)
+    if (ok && n_tiles > 0)
       ok = wait_all(&ctl->o_done[(n_tiles - 1) & 1], ((n_tiles - 1) >> 1) & 1, abort_flag, deadline,
                     a.status, 17, n_tiles);
+    if (ROWS) {
+      row_m = m_used;
+      row_l = ok ? l : -1.f;
+    }
     // Epilogue: O / l as bf16 into the Q buffer (free once the last MMA is
     // done), laid out as the 128-byte-swizzled boxes of the output map, then
     // four TMA stores. A thread owns one row, so direct stores would write
     // 16 bytes per output row per instruction; the staged copy writes whole
     // rows. Rows past the sequence end are clipped by the store.
     unsigned char* sO = sm;  // Q buffer
-    if (VF) {
+    if (ROWS) {
+      // below, once the cluster is through
+    } else if (VF) {
       // fp32 partial O / l of this split and its log2-sum-exp, for the combine
       if (ok) {
         tc::fence_after_sync();
@@ -588,6 +621,87 @@ __global__ void __launch_bounds__(192, 1)
         mbar_wait_bounded_at(&ctl->full[s], (ctl->issued[s] - 1) & 1, &never, dl, a.status, 19,
                              ctl->issued[s], s, ctl->consumed[s]);
   }
+  if constexpr (ROWS) {
+    // Merge: each CTA leaves its O (fp32, rows PITCH bytes apart: an odd number
+    // of 16-byte words, which spreads them over the banks) and (m, l) in its own
+    // Q buffer and ring, and sums every CTA's over its share of the columns.
+    // (Remote reads of whole 128-byte runs; remote writes of a row per lane took
+    // several times as long.)
+    constexpr int PITCH = DV * 4 + 16, ML = BM * PITCH, ALL = ML + BM * 8;
+    const int n = gridDim.x, cols = DV / n, own = blockIdx.x;
+    if (warp >= 2) {
+      const int row = (warp & 3) * 32 + lane;
+      const uint32_t tm = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      if (n_tiles > 0) {
+        tc::fence_after_sync();
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[32];
+          tc::tmem_ld32(tm + COL_O + c * 32, o);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            *reinterpret_cast<uint4*>(sm + row * PITCH + c * 128 + u * 16) =
+                make_uint4(o[u * 4], o[u * 4 + 1], o[u * 4 + 2], o[u * 4 + 3]);
+        }
+      }
+      *reinterpret_cast<float2*>(sm + ML + row * 8) = make_float2(row_m, row_l);
+    }
+    tc::fence_before_sync();
+    __syncwarp();
+    pair::cluster_sync();  // every share is in place
+    const float2* ml = reinterpret_cast<const float2*>(sm + ALL);  // [split][row], copied here
+    for (int i = threadIdx.x; i < n * BM; i += 192) {
+      float x, y;
+      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                   : "=f"(x), "=f"(y)
+                   : "r"(pair::map_to(base + ML + (i % BM) * 8, i / BM))
+                   : "memory");
+      *reinterpret_cast<float2*>(sm + ALL + i * 8) = make_float2(x, y);
+    }
+    __syncthreads();
+    const int groups = cols / 8;  // 16 bytes of output
+    for (int i = threadIdx.x; i < BM * groups; i += 192) {
+      const int row = i / groups, c = (i - row * groups) * 8, t = t0 + row / G;
+      if (row >= G * a.tokens || t >= a.S) continue;
+      float M = -INFINITY, L = 0.f, x[8];
+      bool fine = true;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = 0.f;
+      for (int r = 0; r < n; ++r) M = fmaxf(M, ml[r * BM + row].x);
+#pragma unroll 4
+      for (int r = 0; r < n; ++r) {
+        const float2 v = ml[r * BM + row];
+        fine = fine && !(v.y < 0.f);  // l < 0: that CTA gave up
+        const uint32_t at = pair::map_to(base + row * PITCH + (own * cols + c) * 4, r);
+        float o[8];
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3])
+                     : "r"(at)
+                     : "memory");
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7])
+                     : "r"(at + 16)
+                     : "memory");
+        const bool some = v.x != -INFINITY;  // else no visible key there, and no O
+        const float w = some ? tc::ex2(v.x - M) : 0.f;
+        L += w * v.y;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] += some ? w * o[e] : 0.f;
+      }
+      if (!fine) continue;
+      const float inv = L > 0.f ? 1.f / L : L;  // NaN stays NaN
+      const int64_t hr = ((int64_t)b * a.S + t) * a.Hq + g * G + row % G;
+      *reinterpret_cast<uint4*>(a.out + hr * D + vh * DV + own * cols + c) =
+          make_uint4(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv),
+                     pack_bf16x2(x[4] * inv, x[5] * inv), pack_bf16x2(x[6] * inv, x[7] * inv));
+      if (a.lse && vh == 0 && own == 0 && c == 0)
+        a.lse[((int64_t)b * a.Hq + g * G + row % G) * a.S + t] =
+            L > 0.f ? (M + __log2f(L)) * 0.69314718055994530942f : -INFINITY;
+    }
+    __syncwarp();
+    pair::cluster_sync();  // no CTA leaves while another reads its shared memory
+  }
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, TMEM_COLS);
@@ -640,6 +754,92 @@ cudaError_t launch_prefill_attn_tc(const PrefillAttnArgs& a, int B, int D, int k
     kern<<<grid, 192, Cfg::SMEM, st>>>(mq, mk, mv, mo, t);
   }
   return cudaGetLastError();
+}
+
+namespace {
+// CTAs per unit of rows and columns (the cluster) of the short-chunk form, 0
+// where the unsplit kernels are to be used: see launch_prefill_attn_rows.
+template <int D>
+int rows_splits(const PrefillAttnArgs& a, int B) {
+  using Cfg = TcCfg<D>;
+  const int per_tile = BM / (a.Hq / a.Hkv);  // tokens per row tile
+  const int64_t units = (int64_t)a.Hkv * Cfg::NV * B * ((a.S + per_tile - 1) / per_tile);
+  const int64_t tiles = std::min<int64_t>(((int64_t)a.window + a.S) / BN + 2 + (a.sinks + BN - 1) / BN,
+                                          (a.key_cap + BN - 1) / BN);
+  // clusters of n CTAs that have their SMs to themselves: 148 / n, and somewhat
+  // fewer as clusters do not cross GPCs (15 of 8, 33 of 4, 74 of 2)
+  const int64_t room = (int64_t)multiprocessors() * 17 / 20;
+  int n = 1;
+  while (n < 8 && units * n * 2 <= room && n < tiles) n *= 2;
+  return n > 1 ? n : 0;
+}
+
+template <int D>
+cudaError_t launch_rows_as(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const TcArgs& t,
+                           int B, int n, cudaStream_t st) {
+  using Cfg = TcCfg<D>;
+  auto kern = k_prefill_tc<D, true, true>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(n, t.Hkv * Cfg::NV * ((t.S + t.tokens - 1) / t.tokens), B);
+  cfg.blockDim = dim3(192);
+  cfg.dynamicSmemBytes = Cfg::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = n;
+  at.val.clusterDim.y = 1;
+  at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, mq, t);
+}
+}  // namespace
+
+int prefill_rows_splits(const PrefillAttnArgs& a, int B, int D) {
+  return D == 256 ? rows_splits<256>(a, B) : rows_splits<512>(a, B);
+}
+
+// A short chunk (window plus sinks, paged cache): see k_prefill_tc.
+cudaError_t launch_prefill_attn_rows(const PrefillAttnArgs& a, int B, int D, int n, cudaStream_t st) {
+  const int G = a.Hq / a.Hkv;
+  const uint64_t E = 2;
+  TcArgs t{};
+  t.tokens = BM / G;
+  CUtensorMap mq, mk, mv;
+  {
+    // q_rot [B][S][Hq][D]: a box is the G heads of one KV head for `tokens` tokens
+    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)a.Hq, (uint64_t)a.S, (uint64_t)B};
+    const uint64_t str[3] = {(uint64_t)D * E, (uint64_t)a.Hq * D * E, (uint64_t)a.S * a.Hq * D * E};
+    const uint32_t box[4] = {64, (uint32_t)G, (uint32_t)t.tokens, 1};
+    if (!make_map_bf16_4d(&mq, a.q_rot, dims, str, box)) return cudaErrorInvalidValue;
+  }
+  {
+    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)a.page_size, (uint64_t)a.Hkv, (uint64_t)a.n_pages};
+    const uint64_t strk[3] = {(uint64_t)a.k.stride_row * E, (uint64_t)a.k.stride_h * E, (uint64_t)a.k.stride_b * E};
+    const uint64_t strv[3] = {(uint64_t)a.v.stride_row * E, (uint64_t)a.v.stride_h * E, (uint64_t)a.v.stride_b * E};
+    const uint32_t bk[4] = {64, (uint32_t)BN, 1, 1}, bv[4] = {64, 64, 1, 1};
+    if (!make_map_bf16_4d(&mk, a.k.ptr, dims, strk, bk) || !make_map_bf16_4d(&mv, a.v.ptr, dims, strv, bv))
+      return cudaErrorInvalidValue;
+  }
+  t.S = a.S;
+  t.window = a.window;
+  t.sinks = a.sinks;
+  t.Hq = a.Hq;
+  t.Hkv = a.Hkv;
+  t.key_cap = a.key_cap;
+  t.seq_lens_before = a.seq_lens_before;
+  t.scale_log2 = a.scale_log2;
+  t.out = a.out;
+  t.lse = a.lse;
+  t.status = a.status;
+  t.wait_ns = a.wait_ns;
+  t.page_table = a.page_table;
+  t.page_size = a.page_size;
+  t.pages_per_seq = a.pages_per_seq;
+  t.n_pages = a.n_pages;
+  return D == 256 ? launch_rows_as<256>(mq, mk, mv, t, B, n, st) : launch_rows_as<512>(mq, mk, mv, t, B, n, st);
 }
 
 namespace {

@@ -53,15 +53,17 @@ def attend64(q, K, V, pos, window, sinks, scale):
     before any arithmetic, so NaN there does not matter."""
     n, Hq, D = q.shape
     G = Hq // K.shape[1]
+    p = torch.tensor(pos)[:, None]
+    j = torch.arange(max(pos) + 1)
+    see = (j <= p) & ((j > p - window) | (j < sinks))
+    keys = see.any(0).nonzero().flatten()
+    see, k, v = see[:, keys], K[keys].double(), V[keys].double()
     out = torch.zeros(n, Hq, D, dtype=torch.float64)
     lse = torch.zeros(n, Hq, dtype=torch.float64)
-    for i, p in enumerate(pos):
-        keys = [j for j in range(p + 1) if sees(j, p, window, sinks)]
-        k, v = K[keys].double(), V[keys].double()
-        for h in range(Hq):
-            s = (k[:, h // G] @ q[i, h].double()) * scale
-            lse[i, h] = torch.logsumexp(s, 0)
-            out[i, h] = torch.softmax(s, 0) @ v[:, h // G]
+    for h in range(Hq):
+        s = (q[:, h].double() @ k[:, h // G].T * scale).masked_fill(~see, -math.inf)
+        lse[:, h] = torch.logsumexp(s, 1)
+        out[:, h] = torch.softmax(s, 1) @ v[:, h // G]
     return out, lse
 
 

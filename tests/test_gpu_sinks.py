@@ -247,6 +247,15 @@ def run_prefill(before, S, window, sinks, Hq, Hkv, D, ps, seed=21, keqv=False, s
     assert same_bits(kd.cpu(), kp) and same_bits(vd.cpu(), vp)
 
 
+# enough rows that the keys are not split over a cluster: the unsplit kernels
+PREFILL += [
+    dict(before=[300, 17], S=130, window=150, sinks=9, Hq=16, Hkv=8, D=512, ps=128),   # head pairs
+    dict(before=[0, 260], S=129, window=70, sinks=140, Hq=8, Hkv=8, D=512, ps=128),    # one head per CTA
+    dict(before=[513, 100], S=200, window=128, sinks=1, Hq=16, Hkv=16, D=256, ps=256),
+    dict(before=[90, 600], S=190, window=300, sinks=0, Hq=48, Hkv=16, D=256, ps=128),
+]
+
+
 @pytest.mark.parametrize("case", PREFILL, ids=lambda c: "%s+%d-w%d-s%d-d%d" % (c["before"], c["S"], c["window"],
                                                                                c["sinks"], c["D"]))
 def test_prefill(case):
@@ -257,6 +266,12 @@ def test_prefill(case):
 @pytest.mark.parametrize("D", [256, 512])
 def test_prefill_keqv_and_shared(D, keqv, shared):
     run_prefill([300, 0], 60, window=90, sinks=7, Hq=4, Hkv=1, D=D, ps=128, keqv=keqv, shared=shared, frac=1.0, theta=1e4)
+
+
+@pytest.mark.parametrize("G", range(1, 9))
+def test_prefill_every_group_size(G):
+    """Short chunks pack 128 / G tokens x G heads into a tile."""
+    run_prefill([200, 31], 150 // G + 3, window=80, sinks=5, Hq=2 * G, Hkv=2, D=256 if G % 2 else 512, ps=128)
 
 
 def test_prefill_of_no_tokens_does_nothing():

@@ -650,54 +650,70 @@ __global__ void __launch_bounds__(192, 1)
     tc::fence_before_sync();
     __syncwarp();
     pair::cluster_sync();  // every share is in place
-    const float2* ml = reinterpret_cast<const float2*>(sm + ALL);  // [split][row], copied here
-    for (int i = threadIdx.x; i < n * BM; i += 192) {
-      float x, y;
-      asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-                   : "=f"(x), "=f"(y)
-                   : "r"(pair::map_to(base + ML + (i % BM) * 8, i / BM))
-                   : "memory");
-      *reinterpret_cast<float2*>(sm + ALL + i * 8) = make_float2(x, y);
+    // per row: every split's weight 2^(m - M) / L, then 0 (fine) or 1 (a CTA gave up), M and L
+    float* wgt = reinterpret_cast<float*>(sm + ALL);  // [row][12]
+    if (threadIdx.x < BM) {
+      const int row = threadIdx.x;
+      float2 v[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        v[r] = make_float2(-INFINITY, 0.f);
+        if (r < n)
+          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                       : "=f"(v[r].x), "=f"(v[r].y)
+                       : "r"(pair::map_to(base + ML + row * 8, r)));
+      }
+      float M = -INFINITY, L = 0.f, bad = 0.f;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        M = fmaxf(M, v[r].x);
+        if (v[r].y < 0.f) bad = 1.f;  // l < 0: that CTA gave up
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        v[r].x = v[r].x == -INFINITY ? 0.f : tc::ex2(v[r].x - M);  // no visible key there
+        L += v[r].x * v[r].y;
+      }
+      const float inv = L > 0.f ? 1.f / L : L;  // NaN stays NaN
+#pragma unroll
+      for (int r = 0; r < 8; ++r) wgt[row * 12 + r] = v[r].x * inv;
+      wgt[row * 12 + 8] = bad;
+      const int t = t0 + row / G;
+      if (a.lse && vh == 0 && own == 0 && row < G * a.tokens && t < a.S && bad == 0.f)
+        a.lse[((int64_t)b * a.Hq + g * G + row % G) * a.S + t] =
+            L > 0.f ? (M + __log2f(L)) * 0.69314718055994530942f : -INFINITY;
     }
     __syncthreads();
     const int groups = cols / 8;  // 16 bytes of output
     for (int i = threadIdx.x; i < BM * groups; i += 192) {
       const int row = i / groups, c = (i - row * groups) * 8, t = t0 + row / G;
-      if (row >= G * a.tokens || t >= a.S) continue;
-      float M = -INFINITY, L = 0.f, x[8];
-      bool fine = true;
+      if (row >= G * a.tokens || t >= a.S || wgt[row * 12 + 8] != 0.f) continue;
+      const uint32_t at = base + row * PITCH + (own * cols + c) * 4;
+      float o[8][8], x[8];  // all reads on their way before the first sum
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < n) {
+          const uint32_t from = pair::map_to(at, r);
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(o[r][0]), "=f"(o[r][1]), "=f"(o[r][2]), "=f"(o[r][3])
+                       : "r"(from));
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(o[r][4]), "=f"(o[r][5]), "=f"(o[r][6]), "=f"(o[r][7])
+                       : "r"(from + 16));
+        }
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = 0.f;
-      for (int r = 0; r < n; ++r) M = fmaxf(M, ml[r * BM + row].x);
-#pragma unroll 4
-      for (int r = 0; r < n; ++r) {
-        const float2 v = ml[r * BM + row];
-        fine = fine && !(v.y < 0.f);  // l < 0: that CTA gave up
-        const uint32_t at = pair::map_to(base + row * PITCH + (own * cols + c) * 4, r);
-        float o[8];
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3])
-                     : "r"(at)
-                     : "memory");
-        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7])
-                     : "r"(at + 16)
-                     : "memory");
-        const bool some = v.x != -INFINITY;  // else no visible key there, and no O
-        const float w = some ? tc::ex2(v.x - M) : 0.f;
-        L += w * v.y;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] += some ? w * o[e] : 0.f;
+      for (int r = 0; r < 8; ++r) {
+        const float w = wgt[row * 12 + r];
+        if (r < n && w != 0.f)  // a split without a weight may have left no O
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] += w * o[r][e];
       }
-      if (!fine) continue;
-      const float inv = L > 0.f ? 1.f / L : L;  // NaN stays NaN
       const int64_t hr = ((int64_t)b * a.S + t) * a.Hq + g * G + row % G;
       *reinterpret_cast<uint4*>(a.out + hr * D + vh * DV + own * cols + c) =
-          make_uint4(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv),
-                     pack_bf16x2(x[4] * inv, x[5] * inv), pack_bf16x2(x[6] * inv, x[7] * inv));
-      if (a.lse && vh == 0 && own == 0 && c == 0)
-        a.lse[((int64_t)b * a.Hq + g * G + row % G) * a.S + t] =
-            L > 0.f ? (M + __log2f(L)) * 0.69314718055994530942f : -INFINITY;
+          make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                     pack_bf16x2(x[6], x[7]));
     }
     __syncwarp();
     pair::cluster_sync();  // no CTA leaves while another reads its shared memory

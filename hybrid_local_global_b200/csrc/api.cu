@@ -634,6 +634,7 @@ static int prefill_impl(const void* q, const void* k_new, const void* v_new, voi
   aa.window = window;
   aa.Hq = n_q_heads;
   aa.Hkv = n_kv_heads;
+  aa.sinks = -1;
   aa.scale_log2 = 1.0f;  // already applied to the rotated queries
   aa.out = static_cast<bf16*>(out);
   aa.lse = lse;
@@ -1136,7 +1137,15 @@ int gemma_attn_prefill_sinks(const void* q, const void* k_new, const void* v_new
   ra.Hkv = n_kv_heads;
   ra.n_rot = rope_rotated_pairs(head_dim, rope_frac);
   ra.log2_theta = std::log2((double)rope_theta);
-  ra.q_scale = (float)((double)scale * 1.4426950408889634);
+  // scale * log2(e) = +-2^e * c, 1 <= c < 2: the queries take the sign and the
+  // power of two, which leave their bits alone, the attention kernel takes c
+  // (tiny scales, whose power of two would take the queries below the normal
+  // numbers, go to the queries whole)
+  int e2 = 0;
+  const double lg = (double)scale * 1.4426950408889634;
+  const bool split = std::fabs(lg) > 1e-30;
+  const double c = split ? 2.0 * std::frexp(std::fabs(lg), &e2) : 1.0;
+  ra.q_scale = split ? (float)std::copysign(std::ldexp(1.0, e2 - 1), lg) : (float)lg;
   ra.page_table = page_table;
   ra.page_size = page_size;
   ra.pages_per_seq = pages_per_seq;
@@ -1162,7 +1171,7 @@ int gemma_attn_prefill_sinks(const void* q, const void* k_new, const void* v_new
   aa.sinks = sinks;
   aa.Hq = n_q_heads;
   aa.Hkv = n_kv_heads;
-  aa.scale_log2 = 1.0f;  // already applied to the rotated queries
+  aa.scale_log2 = (float)c;
   aa.out = static_cast<bf16*>(out);
   aa.lse = lse;
   aa.status = status;

@@ -99,8 +99,9 @@ struct PrefillAttnArgs {
                        // gathered for chunked local prefill); 0: view row = position
   const int32_t* seq_lens_before;  // device [B] or null
   int S, window, Hq, Hkv;
-  int sinks;           // > 0 (cache views, window > 0): positions below it stay visible
-  float scale_log2;    // scale * log2(e)
+  int sinks;           // -1: none; else (cache views, window > 0) positions below it stay visible,
+                       // and the logits are multiplied by scale_log2
+  float scale_log2;    // sinks >= 0: the part of scale * log2(e) that the queries do not carry
   bf16* out;           // [B][S][Hq][D]
   float* lse;          // [B][Hq][S] or null
   int* status;

@@ -98,6 +98,7 @@ struct PairCfg {
 
 struct PairArgs {
   int S, window, Hq, Hkv;
+  float scale_log2;  // SK: factor of the logits
   int sinks;  // SK instances: positions below it stay visible to every query
   int64_t key_cap;
   const int32_t* seq_lens_before;
@@ -124,8 +125,9 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatil
 
 // P = 2^(x - mb) over the 128 logits of one row, packed to bf16 pairs, with
 // eight independent partial sums (and, if TRACK, partial maxima).
-template <bool TRACK>
-__device__ __forceinline__ void exp_row(const uint32_t (&r)[4][32], float mb, uint32_t (&pk)[2][32],
+// SCALED: P = 2^(c x - mb).
+template <bool TRACK, bool SCALED>
+__device__ __forceinline__ void exp_row(const uint32_t (&r)[4][32], float c, float mb, uint32_t (&pk)[2][32],
                                         float (&ls)[8], float (&mx)[8]) {
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
@@ -137,7 +139,7 @@ __device__ __forceinline__ void exp_row(const uint32_t (&r)[4][32], float mb, ui
     const float x0 = __uint_as_float(r[i >> 4][(2 * i) & 31]);
     const float x1 = __uint_as_float(r[i >> 4][(2 * i + 1) & 31]);
     if (TRACK) mx[i & 7] = fmaxf(mx[i & 7], fmaxf(x0, x1));
-    const float p0 = tc::ex2(x0 - mb), p1 = tc::ex2(x1 - mb);
+    const float p0 = tc::ex2(SCALED ? fmaf(x0, c, -mb) : x0 - mb), p1 = tc::ex2(SCALED ? fmaf(x1, c, -mb) : x1 - mb);
     ls[i & 7] += p0 + p1;
     pk[i >> 5][i & 31] = pack_bf16x2(p0, p1);
   }
@@ -401,6 +403,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
     const uint32_t p_ready_addr = pair::map_to(smem_u32(&ctl->p_ready), 0);
     int64_t lo, hi;
     visible_range(pos0 + (row_valid ? q0 + row : a.S - 1), a.window, n_keys, &lo, &hi);
+    // SK: the queries carry a power of two of scale * log2(e), which leaves their
+    // bits alone, and the rest of it (1 <= c < 2) is applied to the logits
+    const float c = SK ? a.scale_log2 : 1.f;
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
     int pv_seen = 0;  // P.V products whose completion this thread has consumed
@@ -439,23 +444,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
       bool need;
       float alpha = 1.f;
       if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
-        const float m_new = fmaxf(m_used, max_row(r));
+        const float m_new = fmaxf(m_used, max_row(r) * c);
         need = m_new > m_used + RESCALE_LOG2 || (m_used == -INFINITY && m_new != -INFINITY);
         if (need) {
           alpha = (m_used == -INFINITY) ? 0.f : tc::ex2(m_used - m_new);
           l *= alpha;
           m_used = m_new;
         }
-        exp_row<false>(r, m_used == -INFINITY ? 0.f : m_used, pk, ls, mx);
+        exp_row<false, SK>(r, c, m_used == -INFINITY ? 0.f : m_used, pk, ls, mx);
       } else {
-        exp_row<true>(r, m_used, pk, ls, mx);
-        const float m_new = fmaxf(m_used, max8(mx));
+        exp_row<true, SK>(r, c, m_used, pk, ls, mx);
+        const float m_new = fmaxf(m_used, max8(mx) * c);
         need = m_new > m_used + RESCALE_LOG2;
         if (need) {
           alpha = tc::ex2(m_used - m_new);
           l *= alpha;
           m_used = m_new;
-          exp_row<false>(r, m_used, pk, ls, mx);
+          exp_row<false, SK>(r, c, m_used, pk, ls, mx);
         }
       }
       if (j >= 1 && __any_sync(0xffffffffu, need)) {
@@ -579,7 +584,7 @@ template <int D>
 cudaError_t launch_pair(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
                         const PairArgs& t, int B, cudaStream_t st) {
   using Cfg = PairCfg<D>;
-  auto kern = t.sinks > 0 ? k_prefill_pair<D, true> : k_prefill_pair<D, false>;
+  auto kern = t.sinks >= 0 ? k_prefill_pair<D, true> : k_prefill_pair<D, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
   if (e != cudaSuccess) return e;
   dim3 grid(2 * t.n_pairs, (t.head_pair ? t.Hq / 2 : t.Hq) * Cfg::NV, B);
@@ -599,6 +604,7 @@ cudaError_t launch_prefill_attn_pair(const PrefillAttnArgs& a, int B, int D, int
   t.S = a.S;
   t.window = a.window;
   t.sinks = a.sinks;
+  t.scale_log2 = a.scale_log2;
   t.Hq = a.Hq;
   t.Hkv = a.Hkv;
   t.key_cap = a.key_cap;

@@ -123,8 +123,9 @@ __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatil
 // P = 2^(x - mb) over the 128 logits of one row, packed to bf16 pairs, with
 // eight independent partial sums (and, if TRACK, partial maxima) so the
 // reductions do not run down one dependency chain.
-template <bool TRACK>
-__device__ __forceinline__ void exp_row(const uint32_t (&r)[4][32], float mb, uint32_t (&pk)[2][32],
+// SCALED: P = 2^(c x - mb).
+template <bool TRACK, bool SCALED>
+__device__ __forceinline__ void exp_row(const uint32_t (&r)[4][32], float c, float mb, uint32_t (&pk)[2][32],
                                         float (&ls)[8], float (&mx)[8]) {
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
@@ -136,7 +137,7 @@ __device__ __forceinline__ void exp_row(const uint32_t (&r)[4][32], float mb, ui
     const float x0 = __uint_as_float(r[i >> 4][(2 * i) & 31]);
     const float x1 = __uint_as_float(r[i >> 4][(2 * i + 1) & 31]);
     if (TRACK) mx[i & 7] = fmaxf(mx[i & 7], fmaxf(x0, x1));
-    const float p0 = tc::ex2(x0 - mb), p1 = tc::ex2(x1 - mb);
+    const float p0 = tc::ex2(SCALED ? fmaf(x0, c, -mb) : x0 - mb), p1 = tc::ex2(SCALED ? fmaf(x1, c, -mb) : x1 - mb);
     ls[i & 7] += p0 + p1;
     pk[i >> 5][i & 31] = pack_bf16x2(p0, p1);
   }
@@ -440,6 +441,9 @@ __global__ void __launch_bounds__(192, 1)
     } else {
       visible_range(pos0 + (row_valid ? q0 + row : a.S - 1), a.window, n_keys, &lo, &hi);
     }
+    // SK: the queries carry a power of two of scale * log2(e), which leaves their
+    // bits alone, and the rest of it (1 <= c < 2) is applied to the logits
+    const float c = SK ? a.scale_log2 : 1.f;
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
     int pv_seen = 0;  // P.V products whose completion this thread has consumed
@@ -481,23 +485,23 @@ __global__ void __launch_bounds__(192, 1)
       bool need;
       float alpha = 1.f;
       if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
-        const float m_new = fmaxf(m_used, max_row(r));
+        const float m_new = fmaxf(m_used, max_row(r) * c);
         need = m_new > m_used + RESCALE_LOG2 || (m_used == -INFINITY && m_new != -INFINITY);
         if (need) {
           alpha = (m_used == -INFINITY) ? 0.f : tc::ex2(m_used - m_new);
           l *= alpha;
           m_used = m_new;
         }
-        exp_row<false>(r, m_used == -INFINITY ? 0.f : m_used, pk, ls, mx);
+        exp_row<false, SK>(r, c, m_used == -INFINITY ? 0.f : m_used, pk, ls, mx);
       } else {
-        exp_row<true>(r, m_used, pk, ls, mx);
-        const float m_new = fmaxf(m_used, max8(mx));
+        exp_row<true, SK>(r, c, m_used, pk, ls, mx);
+        const float m_new = fmaxf(m_used, max8(mx) * c);
         need = m_new > m_used + RESCALE_LOG2;
         if (need) {
           alpha = tc::ex2(m_used - m_new);
           l *= alpha;
           m_used = m_new;
-          exp_row<false>(r, m_used, pk, ls, mx);
+          exp_row<false, SK>(r, c, m_used, pk, ls, mx);
         }
       }
       if (j >= 1 && __any_sync(0xffffffffu, need)) {
@@ -754,7 +758,7 @@ cudaError_t launch_prefill_attn_tc(const PrefillAttnArgs& a, int B, int D, int k
   t.n_qtiles = (a.S + BM - 1) / BM;
   if (D == 256) {
     using Cfg = TcCfg<256>;
-    auto kern = a.sinks > 0 ? k_prefill_tc<256, false, true> : k_prefill_tc<256, false, false>;
+    auto kern = a.sinks >= 0 ? k_prefill_tc<256, false, true> : k_prefill_tc<256, false, false>;
     cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
     if (e != cudaSuccess) return e;
@@ -762,7 +766,7 @@ cudaError_t launch_prefill_attn_tc(const PrefillAttnArgs& a, int B, int D, int k
     kern<<<grid, 192, Cfg::SMEM, st>>>(mq, mk, mv, mo, t);
   } else {
     using Cfg = TcCfg<512>;
-    auto kern = a.sinks > 0 ? k_prefill_tc<512, false, true> : k_prefill_tc<512, false, false>;
+    auto kern = a.sinks >= 0 ? k_prefill_tc<512, false, true> : k_prefill_tc<512, false, false>;
     cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
     if (e != cudaSuccess) return e;

@@ -202,7 +202,8 @@ PREFILL = [
 ]
 
 
-def run_prefill(before, S, window, sinks, Hq, Hkv, D, ps, seed=21, keqv=False, shared=False, frac=0.25, theta=1e6):
+def run_prefill(before, S, window, sinks, Hq, Hkv, D, ps, seed=21, keqv=False, shared=False, frac=0.25, theta=1e6,
+                scale=None):
     lens = before or [0, 0]
     B, pps = len(lens), (max(lens) + S) // ps + 2
     held = [sorted(kept_pages(n, window, sinks, ps) | set(range(n // ps, (n + S - 1) // ps + 1))) for n in lens]
@@ -215,14 +216,13 @@ def run_prefill(before, S, window, sinks, Hq, Hkv, D, ps, seed=21, keqv=False, s
     kd, vd = kp.to(DEV), vp.to(DEV)
     out = torch.full((B, S, Hq, D), float("nan"), dtype=torch.bfloat16, device=DEV)
     lse = torch.empty(B, Hq, S, dtype=torch.float32, device=DEV)
-    scale = D ** -0.5
+    scale = D ** -0.5 if scale is None else scale
     flags = (native.GEMMA_F_SHARED if shared else 0) | (native.GEMMA_F_KEQV if keqv else 0)
     native.gemma_attn_prefill_sinks(
         q.to(DEV), None if shared else kn.to(DEV), None if shared or keqv else vn.to(DEV), kd, None if keqv else vd,
         table.to(DEV), window=window, sinks=sinks, rope_frac=frac, rope_theta=theta, scale=scale, out=out, lse=lse,
         seq_lens_before=None if before is None else torch.tensor(before, dtype=torch.int32, device=DEV), flags=flags)
     assert native.gemma_attn_sync_status() == 0, native.gemma_last_error()
-    mult = float(np.float32(scale * 1.4426950408889634))
     for b, n in enumerate(lens):
         pos = list(range(n, n + S))
         if not shared:
@@ -235,8 +235,8 @@ def run_prefill(before, S, window, sinks, Hq, Hkv, D, ps, seed=21, keqv=False, s
                 V[b, j] = got if keqv else vn[b, i]
                 if not keqv:
                     vp[page, :, row] = vn[b, i]
-        # queries carry scale * log2(e) and are rounded once
-        qr = bf16(rope64(q[b], pos, frac, theta) * mult).double() / mult
+        # the queries are rounded once, as they are up to a power of two
+        qr = bf16(rope64(q[b], pos, frac, theta))
         ref, ref_lse = attend64(qr, K[b], V[b], pos, window, sinks, scale)
         got = out[b].double().cpu()
         assert torch.isfinite(got).all()
@@ -272,6 +272,13 @@ def test_prefill_keqv_and_shared(D, keqv, shared):
 def test_prefill_every_group_size(G):
     """Short chunks pack 128 / G tokens x G heads into a tile."""
     run_prefill([200, 31], 150 // G + 3, window=80, sinks=5, Hq=2 * G, Hkv=2, D=256 if G % 2 else 512, ps=128)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.03, 0.5, 2.0 ** -6, 1e-30])
+@pytest.mark.parametrize("D", [256, 512])
+def test_prefill_scales(D, scale):
+    run_prefill([100], 40, window=60, sinks=3, Hq=4, Hkv=1, D=D, ps=128, scale=scale)
+    run_prefill([100, 0], 130, window=60, sinks=3, Hq=16, Hkv=16, D=D, ps=128, scale=scale)
 
 
 def test_prefill_of_no_tokens_does_nothing():

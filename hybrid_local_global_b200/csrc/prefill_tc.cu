@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(192, 1)
     }
     // SK: the queries carry a power of two of scale * log2(e), which leaves their
     // bits alone, and the rest of it (1 <= c < 2) is applied to the logits
-    const float c = SK ? a.scale_log2 : 1.f;
+    const float factor = SK ? a.scale_log2 : 1.f;
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
     int pv_seen = 0;  // P.V products whose completion this thread has consumed
@@ -485,23 +485,23 @@ __global__ void __launch_bounds__(192, 1)
       bool need;
       float alpha = 1.f;
       if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
-        const float m_new = fmaxf(m_used, max_row(r) * c);
+        const float m_new = fmaxf(m_used, max_row(r) * factor);
         need = m_new > m_used + RESCALE_LOG2 || (m_used == -INFINITY && m_new != -INFINITY);
         if (need) {
           alpha = (m_used == -INFINITY) ? 0.f : tc::ex2(m_used - m_new);
           l *= alpha;
           m_used = m_new;
         }
-        exp_row<false, SK>(r, c, m_used == -INFINITY ? 0.f : m_used, pk, ls, mx);
+        exp_row<false, SK>(r, factor, m_used == -INFINITY ? 0.f : m_used, pk, ls, mx);
       } else {
-        exp_row<true, SK>(r, c, m_used, pk, ls, mx);
-        const float m_new = fmaxf(m_used, max8(mx) * c);
+        exp_row<true, SK>(r, factor, m_used, pk, ls, mx);
+        const float m_new = fmaxf(m_used, max8(mx) * factor);
         need = m_new > m_used + RESCALE_LOG2;
         if (need) {
           alpha = tc::ex2(m_used - m_new);
           l *= alpha;
           m_used = m_new;
-          exp_row<false, SK>(r, c, m_used, pk, ls, mx);
+          exp_row<false, SK>(r, factor, m_used, pk, ls, mx);
         }
       }
       if (j >= 1 && __any_sync(0xffffffffu, need)) {

@@ -294,7 +294,6 @@ int record_error(int code, const char* msg) { return fail(code, "%s", msg); }
 int record_ok() { return succeed(); }
 int* device_status() { return status_ptr(); }
 int multiprocessors() { return sm_count(); }
-unsigned long long wait_limit_ns() { return (unsigned long long)g_wait_ns.load(); }
 void half_turn_ladder(double step, int n, double* out) {
   double coarse[16], fine[16];
   for (int i = 0; i < 16; ++i) {

@@ -149,7 +149,6 @@ int record_error(int code, const char* msg);  // sets gemma_last_error(), return
 int record_ok();                              // clears it, returns GEMMA_OK
 int* device_status();                         // the current device's status word, or null
 int multiprocessors();                        // of the current device
-unsigned long long wait_limit_ns();           // of bounded device waits
 // out[i] = 2^(-i * step) / pi, i < n <= 256: frequencies in half-turns per
 // position. Two tables of 16 powers and one product each (an exp2 per entry
 // would be most of a small call's host time).

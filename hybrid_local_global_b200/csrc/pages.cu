@@ -18,6 +18,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "pair.cuh"
 
 namespace hlg {
@@ -270,6 +271,7 @@ __device__ __forceinline__ void reserve_plan(const Book& bk, const int32_t* __re
 __global__ void __launch_bounds__(PLAN_T) k_pages_reserve(Book bk, const int32_t* __restrict__ seq_lens,
                                                           const int32_t* __restrict__ new_tokens,
                                                           int32_t* lacking, ReservePlan ws, int* status) {
+  let_next_start();  // the copies'
   reserve_plan(bk, seq_lens, new_tokens, lacking, ws, status);
 }
 
@@ -287,6 +289,7 @@ struct CompactPlan {
 
 __global__ void __launch_bounds__(PLAN_T) k_pages_compact(Book bk, CompactPlan ws, int32_t* n_live) {
   extern __shared__ uint32_t live_s[];  // one bit per page
+  let_next_start();  // the copies'
   const int tid = threadIdx.x, lane = tid & 31;
   const int n_words = (bk.n_pages + 31) / 32;
   int cnt = 0;
@@ -433,6 +436,7 @@ __device__ __forceinline__ void copy_tiles(const CopyList& a, const Seg* seg, in
 template <int N>
 __global__ void __launch_bounds__(COPY_T) k_pages_copy(const __grid_constant__ CopyArgs<N> a, const Book bk,
                                                        const int32_t* __restrict__ map) {
+  after_previous();  // the plan
   if (map) {
     const int64_t n = (int64_t)bk.n_seqs * bk.pps;
     for (int64_t i = (int64_t)blockIdx.x * COPY_T + threadIdx.x; i < n; i += (int64_t)gridDim.x * COPY_T) {
@@ -536,7 +540,9 @@ cudaError_t launch_copy(const CopyList& list, const Seg* seg, int64_t work, cons
   std::copy(seg, seg + list.n_segs, a.seg);
   // 32 CTAs per SM in all (256 MB: 42 us, 92 % of the copy rate; 8 per SM: 45)
   const int64_t grid = std::min<int64_t>(work, (int64_t)multiprocessors() * 32);
-  k_pages_copy<N><<<(unsigned)std::max<int64_t>(grid, 1), COPY_T, 0, st>>>(a, bk, map);
+  const dim3 ctas((unsigned)std::max<int64_t>(grid, 1));
+  if (list.n_dev) return launch_early(k_pages_copy<N>, ctas, COPY_T, 0, st, 0, a, bk, map);
+  k_pages_copy<N><<<ctas, COPY_T, 0, st>>>(a, bk, map);
   return cudaGetLastError();
 }
 

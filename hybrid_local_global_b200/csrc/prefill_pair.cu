@@ -46,6 +46,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "pair.cuh"
 #include "tc.cuh"
 #include "tmap.h"
@@ -210,7 +211,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
   const int64_t n_keys = pos0 + a.S;
   // view row of a key = its position - koff (a gathered key window starts at pos0 - window)
   const int64_t koff = a.key_off_window ? pos0 - a.window : 0;
-  if (pos0 < 0 || n_keys - koff > a.key_cap) return;  // reported by the RoPE kernel; same for both CTAs
+  if (pos0 < 0 || n_keys - koff > a.key_cap) {  // reported by the RoPE kernel; same for both CTAs
+    if (SK) after_previous();
+    return;
+  }
   int64_t lo_first, hi_first, lo_last, hi_last;
   visible_range(pos0 + pq0, a.window, n_keys, &lo_first, &hi_first);
   visible_range(pos0 + min(pq0 + span - 1, a.S - 1), a.window, n_keys, &lo_last, &hi_last);
@@ -248,6 +252,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
     pair::tmem_alloc2(smem_u32(&ctl->tmem_base), TMEM_COLS);
     pair::tmem_relinquish2();
   }
+  if (SK) after_previous();  // the rotation, beside which all of the above ran
   tc::fence_before_sync();
   __syncwarp();
   pair::cluster_sync();  // both CTAs' barriers exist before any remote arrive or commit
@@ -588,6 +593,7 @@ cudaError_t launch_pair(const CUtensorMap& mq, const CUtensorMap& mk, const CUte
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
   if (e != cudaSuccess) return e;
   dim3 grid(2 * t.n_pairs, (t.head_pair ? t.Hq / 2 : t.Hq) * Cfg::NV, B);
+  if (t.sinks >= 0) return launch_early(kern, grid, 192, Cfg::SMEM, st, 0, mq, mk, mv, mo, t);
   kern<<<grid, 192, Cfg::SMEM, st>>>(mq, mk, mv, mo, t);
   return cudaGetLastError();
 }

@@ -43,6 +43,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "pair.cuh"
 #include "tc.cuh"
 #include "tmap.h"
@@ -219,7 +220,10 @@ __global__ void __launch_bounds__(192, 1)
   // view row of a key = its position - koff (a gathered key window starts at pos0 - window)
   const int64_t koff = (!VF && a.key_off_window) ? pos0 - a.window : 0;
   if (!VF || SK) {
-    if (pos0 < 0 || n_keys - koff > a.key_cap) return;  // reported by the RoPE kernel
+    if (pos0 < 0 || n_keys - koff > a.key_cap) {  // reported by the RoPE kernel
+      if (SK) after_previous();
+      return;
+    }
     const int first = ROWS ? t0 : q0, last = min(ROWS ? t0 + a.tokens - 1 : q0 + BM - 1, a.S - 1);
     int64_t lo_first, hi_first, lo_last, hi_last;
     visible_range(pos0 + first, a.window, n_keys, &lo_first, &hi_first);
@@ -266,6 +270,7 @@ __global__ void __launch_bounds__(192, 1)
     tc::tmem_alloc(smem_u32(&ctl->tmem_base), TMEM_COLS);
     tc::tmem_relinquish();
   }
+  if (SK) after_previous();  // the rotation, beside which all of the above ran
   tc::fence_before_sync();
   __syncwarp();
   __syncthreads();
@@ -763,6 +768,7 @@ cudaError_t launch_prefill_attn_tc(const PrefillAttnArgs& a, int B, int D, int k
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
     if (e != cudaSuccess) return e;
     dim3 grid(a.Hq * Cfg::NV, B, t.n_qtiles);
+    if (a.sinks >= 0) return launch_early(kern, grid, 192, Cfg::SMEM, st, 0, mq, mk, mv, mo, t);
     kern<<<grid, 192, Cfg::SMEM, st>>>(mq, mk, mv, mo, t);
   } else {
     using Cfg = TcCfg<512>;
@@ -771,6 +777,7 @@ cudaError_t launch_prefill_attn_tc(const PrefillAttnArgs& a, int B, int D, int k
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
     if (e != cudaSuccess) return e;
     dim3 grid(a.Hq * Cfg::NV, B, t.n_qtiles);
+    if (a.sinks >= 0) return launch_early(kern, grid, 192, Cfg::SMEM, st, 0, mq, mk, mv, mo, t);
     kern<<<grid, 192, Cfg::SMEM, st>>>(mq, mk, mv, mo, t);
   }
   return cudaGetLastError();
@@ -801,19 +808,8 @@ cudaError_t launch_rows_as(const CUtensorMap& mq, const CUtensorMap& mk, const C
   auto kern = k_prefill_tc<D, true, true>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(n, t.Hkv * Cfg::NV * ((t.S + t.tokens - 1) / t.tokens), B);
-  cfg.blockDim = dim3(192);
-  cfg.dynamicSmemBytes = Cfg::SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = n;
-  at.val.clusterDim.y = 1;
-  at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, mq, t);
+  const dim3 grid(n, t.Hkv * Cfg::NV * ((t.S + t.tokens - 1) / t.tokens), B);
+  return launch_early(kern, grid, 192, Cfg::SMEM, st, n, mq, mk, mv, mq, t);
 }
 }  // namespace
 

@@ -24,6 +24,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 
 namespace hlg {
 
@@ -139,6 +140,7 @@ constexpr int ROPE_MIN_CTAS = 512;  // this many CTAs (about 3.5 per SM): then o
 // rows window.. of the K and V windows (a.win_rows rows per sequence).
 template <int D, bool WIN>
 __global__ void __launch_bounds__(256, 2) k_prefill_rope(PrefillRopeArgs a) {
+  let_next_start();
   const int b = blockIdx.y;
   const int e0 = threadIdx.x * 8;
   const int64_t pos0 = a.seq_lens_before ? (int64_t)a.seq_lens_before[b] : 0;

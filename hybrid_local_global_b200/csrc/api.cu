@@ -1179,15 +1179,15 @@ int gemma_attn_prefill_sinks(const void* q, const void* k_new, const void* v_new
   aa.page_size = page_size;
   aa.pages_per_seq = pages_per_seq;
   aa.n_pages = n_pages;
-  // head_dim 512 with an even number of q heads per KV head: head pairs, as
-  // in gemma_attn_prefill
-  const bool pair = head_dim == 512 && (n_q_heads / n_kv_heads) % 2 == 0;
+  // head_dim 256, and 512 with an even number of q heads per KV head: pairs of
+  // heads (256 with an odd number: of row tiles)
+  const bool even = (n_q_heads / n_kv_heads) % 2 == 0;
   {
     ProfScope p_attn(GEMMA_KERNEL_PREFILL_ATTN, st);
     const int splits = prefill_rows_splits(aa, batch, head_dim);
     e = splits ? launch_prefill_attn_rows(aa, batch, head_dim, splits, st)
-        : pair ? launch_prefill_attn_pair(aa, batch, head_dim, page_size, 0, 1, st)
-               : launch_prefill_attn_tc(aa, batch, head_dim, page_size, 0, st);
+        : even || head_dim == 256 ? launch_prefill_attn_pair(aa, batch, head_dim, page_size, 0, even, st)
+                                  : launch_prefill_attn_tc(aa, batch, head_dim, page_size, 0, st);
     p_attn.done();
   }
   if (e != cudaSuccess) return cuda_fail(e, "prefill attention launch");

@@ -69,7 +69,7 @@ struct Ctl {
   uint64_t full[NSTAGE];
   uint64_t empty[NSTAGE];
   uint64_t s_full[2];
-  uint64_t p_ready;
+  uint64_t p_ready[2];  // SK: P_j completes phase j/2 of p_ready[j % 2]; else phase j of p_ready[0]
   uint64_t o_done[2];  // PV_i completes phase i/2 of o_done[i % 2]
   uint64_t drain;
   uint32_t tmem_base;
@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(192, 1)
     }
     mbar_init(&ctl->s_full[0], 1);
     mbar_init(&ctl->s_full[1], 1);
-    mbar_init(&ctl->p_ready, 128);
+    mbar_init(&ctl->p_ready[0], 128);
+    mbar_init(&ctl->p_ready[1], 128);
     mbar_init(&ctl->o_done[0], 1);
     mbar_init(&ctl->o_done[1], 1);
     mbar_init(&ctl->drain, 1);
@@ -383,7 +384,8 @@ __global__ void __launch_bounds__(192, 1)
         tc::commit_if(go, smem_u32(&ctl->s_full[j & 1]));
       }
       if (j >= 1) {
-        if (!wait_all(&ctl->p_ready, (j - 1) & 1, abort_flag, deadline, a.status, 13, j)) {
+        if (!wait_all(&ctl->p_ready[SK ? (j - 1) & 1 : 0], (SK ? (j - 1) >> 1 : j - 1) & 1, abort_flag, deadline, a.status,
+                      13, j)) {
           ok = false;
           break;
         }
@@ -469,16 +471,25 @@ __global__ void __launch_bounds__(192, 1)
       // visible range need it).
       if (!((kb >= lo || (SK && kb + BN <= a.sinks)) && kb + BN - 1 <= hi)) {
         const int64_t dlo = lo - kb, dhi = hi - kb;
-        const int c_lo = (int)(dlo < -1 ? -1 : dlo);
+        const int c_lo = (int)(dlo < -1 ? -1 : dlo > BN ? BN : dlo);
         const int c_hi = (int)(dhi > BN ? BN : dhi);
-        const int c_sink = SK ? (int)(a.sinks - kb > BN ? BN : a.sinks - kb) : 0;  // columns below it are sinks
+        const int c_sink = SK ? (int)(a.sinks - kb > BN ? BN : a.sinks - kb < 0 ? 0 : a.sinks - kb) : 0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c) {
+          if (SK) {
+            // bits, not comparisons per element: three of ten tiles of a window of 1024 are
+            // edge tiles, and each took 6000 cycles with chains of predicates, 2000 without
+            const uint32_t vis = tc::visible_bits(c * 32, c_lo, c_hi, c_sink);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int col = c * 32 + e;
-            if ((col < c_lo && !(SK && col < c_sink)) || col > c_hi) r[c][e] = __float_as_uint(-INFINITY);
+            for (int e = 0; e < 32; ++e) r[c][e] = vis >> e & 1u ? r[c][e] : __float_as_uint(-INFINITY);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int col = c * 32 + e;
+              if (col < c_lo || col > c_hi) r[c][e] = __float_as_uint(-INFINITY);
+            }
           }
+        }
       }
       // The running max m_used only moves when a tile's max exceeds it by more
       // than 2^8 (or on a row's first visible key), so P = 2^(x - m_used) is
@@ -534,8 +545,11 @@ __global__ void __launch_bounds__(192, 1)
       tc::tmem_st32(s_tm, pk[0]);
       tc::tmem_st32(s_tm + 32, pk[1]);
       // consume P_{j-1} V_{j-1} before P_{j+1} V_{j+1} can complete the next
-      // phase of the same barrier (parity waits must not fall two behind)
-      if (j >= 1 && pv_seen < j) {
+      // phase of the same barrier (parity waits must not fall two behind). SK:
+      // after P_j is released, so that P_j V_j does not wait for the news of
+      // P_{j-1} V_{j-1} to come here and go back; P_j's arrival may then overtake
+      // the issuer's wait for P_{j-1}, hence a barrier per buffer of P
+      if (!SK && j >= 1 && pv_seen < j) {
         if (!wait_all(&ctl->o_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, deadline, a.status, 16, j)) {
           ok = false;
           break;
@@ -544,7 +558,14 @@ __global__ void __launch_bounds__(192, 1)
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
-      mbar_arrive(&ctl->p_ready);
+      mbar_arrive(&ctl->p_ready[SK ? j & 1 : 0]);
+      if (SK && j >= 1 && pv_seen < j) {
+        if (!wait_all(&ctl->o_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, deadline, a.status, 16, j)) {
+          ok = false;
+          break;
+        }
+        pv_seen = j;
+      }
     }
     if (ok && n_tiles > 0)
       ok = wait_all(&ctl->o_done[(n_tiles - 1) & 1], ((n_tiles - 1) >> 1) & 1, abort_flag, deadline,
@@ -763,12 +784,12 @@ cudaError_t launch_prefill_attn_tc(const PrefillAttnArgs& a, int B, int D, int k
   t.n_qtiles = (a.S + BM - 1) / BM;
   if (D == 256) {
     using Cfg = TcCfg<256>;
-    auto kern = a.sinks >= 0 ? k_prefill_tc<256, false, true> : k_prefill_tc<256, false, false>;
+    if (a.sinks >= 0) return cudaErrorInvalidValue;  // launch_prefill_attn_pair's
+    auto kern = k_prefill_tc<256, false, false>;
     cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
     if (e != cudaSuccess) return e;
     dim3 grid(a.Hq * Cfg::NV, B, t.n_qtiles);
-    if (a.sinks >= 0) return launch_early(kern, grid, 192, Cfg::SMEM, st, 0, mq, mk, mv, mo, t);
     kern<<<grid, 192, Cfg::SMEM, st>>>(mq, mk, mv, mo, t);
   } else {
     using Cfg = TcCfg<512>;

@@ -39,6 +39,8 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* m, uint32_t smem
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // wait until the bulk stores of this thread have finished reading shared memory
 __device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// all but the last of them
+__device__ __forceinline__ void bulk_wait_read1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 
 // ---------------------------------------------------------------- descriptors
 // Shared-memory matrix descriptor (tcgen05): start address, leading and
@@ -191,6 +193,14 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// The 32 columns c0 .. c0 + 31 of a logits tile that a row sees, one bit each:
+// those below `sink` and those from lo on, up to hi (tile columns).
+__device__ __forceinline__ uint32_t visible_bits(int c0, int lo, int hi, int sink) {
+  const int l = min(max(lo - c0, 0), 32), h = min(max(hi + 1 - c0, 0), 32), k = min(max(sink - c0, 0), 32);
+  const uint32_t from = l < 32 ? ~0u << l : 0u, upto = h < 32 ? (1u << h) - 1u : ~0u, sinks = k < 32 ? (1u << k) - 1u : ~0u;
+  return (from | sinks) & upto;
 }
 
 }  // namespace tc

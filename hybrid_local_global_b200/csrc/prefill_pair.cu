@@ -618,17 +618,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
 // (which its first P V waits for), through 32 KB of shared memory of its own.
 // ---------------------------------------------------------------------------
 constexpr int STREAM_Q = BM * 256 * 2;
-constexpr int STREAM_OUT = 32768;  // per softmax warp, two boxes of 32 rows x 64 columns
-constexpr int STREAM_NS = (SMEM_MAX - ALIGN_B - STREAM_Q - STREAM_OUT - 1024) / STAGE_B;  // 4
-constexpr int STREAM_SMEM = ALIGN_B + STREAM_Q + STREAM_OUT + STREAM_NS * STAGE_B + 1024;
+constexpr int STREAM_WARPS = 8;    // softmax warps
+constexpr int STREAM_BOX = 4096;   // output box of a softmax warp: 32 rows x 64 columns
+constexpr int STREAM_OUT = STREAM_WARPS * STREAM_BOX;
+constexpr int STREAM_T = 64 + 32 * STREAM_WARPS;
+constexpr int STREAM_NS = (SMEM_MAX - ALIGN_B - STREAM_Q - STREAM_OUT - 2048) / STAGE_B;  // 4
+constexpr int STREAM_SMEM = ALIGN_B + STREAM_Q + STREAM_OUT + STREAM_NS * STAGE_B + 2048;
 static_assert(STREAM_NS >= 3 && STREAM_SMEM <= SMEM_MAX, "shared memory plan");
 
 struct StreamCtl {
   Ctl<STREAM_NS> ring;  // q_full and the others' phases run on from row tile to row tile
   uint64_t q_empty;     // the row tile's last S is done
-  uint64_t o_free;      // leader: the row tile's output left TMEM (4 local + 4 peer warps)
+  uint64_t o_free;      // leader: the row tile's output left TMEM (8 local + 8 peer warps)
+  float part[2][BM];    // halves of a row: maxima, sums
 };
-static_assert(sizeof(StreamCtl) <= 1024, "control block");
+static_assert(sizeof(StreamCtl) <= 2048, "control block");
 
 // A pair's row tile(s) and the key tiles it sees.
 struct RowTile {
@@ -661,7 +665,52 @@ __device__ __forceinline__ bool row_tile(const PairArgs& a, int i, int rank, Row
   return true;
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
+// AND or OR of a predicate over the 64 threads of two warps.
+template <bool AND>
+__device__ __forceinline__ bool vote64(int id, bool p) {
+  uint32_t r;
+  if (AND)
+    asm volatile("{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\tbar.red.and.pred po, %2, 64, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
+                 : "=r"(r) : "r"((uint32_t)p), "r"(id) : "memory");
+  else
+    asm volatile("{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\tbar.red.or.pred po, %2, 64, pi;\n\tselp.u32 %0, 1, 0, po;\n\t}"
+                 : "=r"(r) : "r"((uint32_t)p), "r"(id) : "memory");
+  return r != 0;
+}
+
+// exp_row and max_row over half a row.
+template <bool TRACK>
+__device__ __forceinline__ void exp_half(const uint32_t (&r)[2][32], float c, float mb, uint32_t (&pk)[32], float* sum,
+                                         float* top) {
+  float ls[8], mx[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    ls[u] = 0.f;
+    mx[u] = -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float x0 = __uint_as_float(r[i >> 4][(2 * i) & 31]), x1 = __uint_as_float(r[i >> 4][(2 * i + 1) & 31]);
+    if (TRACK) mx[i & 7] = fmaxf(mx[i & 7], fmaxf(x0, x1));
+    const float p0 = tc::ex2(fmaf(x0, c, -mb)), p1 = tc::ex2(fmaf(x1, c, -mb));
+    ls[i & 7] += p0 + p1;
+    pk[i] = pack_bf16x2(p0, p1);
+  }
+  *sum = ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
+  if (TRACK) *top = max8(mx);
+}
+__device__ __forceinline__ float max_half(const uint32_t (&r)[2][32]) {
+  float mx[8];
+#pragma unroll
+  for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int e = 0; e < 32; ++e) mx[e & 7] = fmaxf(mx[e & 7], __uint_as_float(r[c][e]));
+  return max8(mx);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(STREAM_T, 1)
     k_prefill_stream(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                      const PairArgs a, const int n_items) {
@@ -693,10 +742,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
       mbar_init(&ctl->s_full[u], 1);
       mbar_init(&ctl->o_done[u], 1);
     }
-    for (int u = 0; u < 2; ++u) mbar_init(&ctl->p_ready[u], 8);  // one arrival per softmax warp of either CTA
+    for (int u = 0; u < 2; ++u) mbar_init(&ctl->p_ready[u], 2 * STREAM_WARPS);  // one per softmax warp of either CTA
     mbar_init(&ctl->drain, 1);
     mbar_init(&sc->q_empty, 1);
-    mbar_init(&sc->o_free, 8);
+    mbar_init(&sc->o_free, 2 * STREAM_WARPS);
     ctl->abort = 0;
     ctl->q_issued = 0;
     ctl->q_consumed = 0;
@@ -821,8 +870,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
         const uint32_t p_tm = tmem + COL_S + (uint32_t)(k & 1) * 128;
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
-          pair::mma2_ts_if(go, tmem + COL_O, p_tm + kk * 8, dv + (uint64_t)((s * STAGE_B + kk * 2048) >> 4), IDESC_PV,
-                           (!v_first || kk) ? 1u : 0u);
+          pair::mma2_ts_if(go, tmem + COL_O, p_tm + (kk >> 2) * 64 + (kk & 3) * 8,
+                           dv + (uint64_t)((s * STAGE_B + kk * 2048) >> 4), IDESC_PV, (!v_first || kk) ? 1u : 0u);
         pair::commit2_mc_if(go, smem_u32(&ctl->empty[s]), BOTH);
         pair::commit2_mc_if(go, smem_u32(&ctl->o_done[k & 1]), BOTH);
         return true;
@@ -867,12 +916,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax (both CTAs)
-    const int wq = warp & 3;
+    // Two warps per 32 rows, each with half the columns of S and of O. A row's two
+    // threads keep the same maximum: they vote on whether it has to move.
+    const int wq = warp & 3, half = (warp - 2) >> 2;
     const int row = wq * 32 + lane;
     const uint32_t tm = tmem + ((uint32_t)(wq * 32) << 16);
     const uint32_t p_ready_addr = pair::map_to(smem_u32(&ctl->p_ready[0]), 0);
     const uint32_t o_free_addr = pair::map_to(smem_u32(&sc->o_free), 0);
-    unsigned char* out_s = sm + OUT_OFF + wq * (STREAM_OUT / 4);
+    unsigned char* box = sm + OUT_OFF + (warp - 2) * STREAM_BOX;
     // the row tile before, whose output still lies in TMEM
     float out_m = 0.f, out_l = 0.f;
     int out_b = 0, out_h = 0, out_q0 = 0;
@@ -880,12 +931,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
       tc::fence_after_sync();
       const float inv = out_l > 0.f ? 1.f / out_l : 0.f;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = half * 2; c < half * 2 + 2; ++c) {
         uint32_t o[2][32];
         tc::tmem_ld32(tm + COL_O + c * 64, o[0]);
         tc::tmem_ld32(tm + COL_O + c * 64 + 32, o[1]);
         tc::tmem_wait_ld();
-        if (c == 3) {
+        if (c & 1) {
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) {
@@ -895,8 +946,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
               pair::arrive_remote_tmem(o_free_addr);
           }
         }
-        unsigned char* box = out_s + (c & 1) * 4096;
-        if (lane == 0) tc::bulk_wait_read1();  // the store of two boxes ago has read it
+        if (lane == 0) tc::bulk_wait_read0();  // the store before has read the box
         __syncwarp();
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
@@ -917,7 +967,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
         }
         __syncwarp();
       }
-      if (out_q0 + row < a.S && a.lse)
+      if (half == 0 && out_q0 + row < a.S && a.lse)
         a.lse[((int64_t)out_b * a.Hq + out_h) * a.S + out_q0 + row] =
             out_l > 0.f ? (out_m + __log2f(out_l)) * 0.69314718055994530942f : -INFINITY;
     };
@@ -931,6 +981,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
       return wait_all(&ctl->o_done[k & 1], (k >> 1) & 1, abort_flag, deadline, a.status, 58, k, n);
     };
     const float factor = a.scale_log2;
+    // A warp that gave up (ok false) goes on to the next vote, at which both warps leave.
     for (int i = item0; i < n_items && ok; i += step) {
       if (!row_tile(a, i, rank, &t)) continue;
       deadline = globaltimer_ns() + a.wait_ns;
@@ -938,15 +989,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
       int64_t lo, hi;
       visible_range(t.pos0 + (row_valid ? t.q0 + row : a.S - 1), a.window, t.n_keys, &lo, &hi);
       float m_used = -INFINITY, l = 0.f;
+      bool left = false;  // both warps, at a vote
       for (int j = 0; j < t.n_tiles; ++j, ++jt) {
         const int64_t kb = t.key(j);
-        ok = wait_all(&ctl->s_full[jt & 1], (jt >> 1) & 1, abort_flag, deadline, a.status, 57, jt, n);
-        if (!ok) break;
+        ok = ok && wait_all(&ctl->s_full[jt & 1], (jt >> 1) & 1, abort_flag, deadline, a.status, 57, jt, n);
         tc::fence_after_sync();
-        const uint32_t s_tm = tm + COL_S + (uint32_t)(jt & 1) * 128;
-        uint32_t r[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tc::tmem_ld32(s_tm + c * 32, r[c]);
+        const uint32_t s_tm = tm + COL_S + (uint32_t)((jt & 1) * 128 + half * 64);
+        uint32_t r[2][32];
+        tc::tmem_ld32(s_tm, r[0]);
+        tc::tmem_ld32(s_tm + 32, r[1]);
         tc::tmem_wait_ld();
         if (!((kb >= lo || kb + BN <= a.sinks) && kb + BN - 1 <= hi)) {
           const int64_t dlo = lo - kb, dhi = hi - kb;
@@ -954,73 +1005,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
           const int c_hi = (int)(dhi > BN ? BN : dhi);
           const int c_sink = (int)(a.sinks - kb > BN ? BN : a.sinks - kb < 0 ? 0 : a.sinks - kb);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t vis = tc::visible_bits(c * 32, c_lo, c_hi, c_sink);
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t vis = tc::visible_bits(half * 64 + c * 32, c_lo, c_hi, c_sink);
 #pragma unroll
             for (int e = 0; e < 32; ++e) r[c][e] = vis >> e & 1u ? r[c][e] : __float_as_uint(-INFINITY);
           }
         }
-        // as in k_prefill_pair: one speculative pass against the running maximum
-        float mx[8], ls[8];
-        uint32_t pk[2][32];
-        bool need = false;
+        // one speculative pass against the running maximum, unless a row has seen no key yet
+        float mx, ls;
+        uint32_t pk[32];
+        const bool fresh = __any_sync(0xffffffffu, m_used == -INFINITY);
+        if (fresh)
+          mx = max_half(r);
+        else
+          exp_half<true>(r, factor, m_used, pk, &ls, &mx);
         float alpha = 1.f;
-        if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
-          const float m_new = fmaxf(m_used, max_row(r) * factor);
+        bool need = false;
+        if (vote64<false>(1 + wq, !ok || fresh || mx * factor > m_used + RESCALE_LOG2)) {
+          sc->part[half][row] = mx;
+          ok = vote64<true>(1 + wq, ok);
+          left = !ok;
+          if (left) break;
+          const float m_new = fmaxf(m_used, fmaxf(mx, sc->part[half ^ 1][row]) * factor);
           need = m_new > m_used + RESCALE_LOG2 || (m_used == -INFINITY && m_new != -INFINITY);
           if (need) {
             alpha = (m_used == -INFINITY) ? 0.f : tc::ex2(m_used - m_new);
             l *= alpha;
             m_used = m_new;
           }
-          exp_row<false, true>(r, factor, m_used == -INFINITY ? 0.f : m_used, pk, ls, mx);
-        } else {
-          exp_row<true, true>(r, factor, m_used, pk, ls, mx);
-          const float m_new = fmaxf(m_used, max8(mx) * factor);
-          need = m_new > m_used + RESCALE_LOG2;
-          if (need) {
-            alpha = tc::ex2(m_used - m_new);
-            l *= alpha;
-            m_used = m_new;
-            exp_row<false, true>(r, factor, m_used, pk, ls, mx);
-          }
+          if (fresh || need) exp_half<false>(r, factor, m_used == -INFINITY ? 0.f : m_used, pk, &ls, &mx);
         }
         if (j >= 1 && __any_sync(0xffffffffu, need)) {
           ok = pv_done(jt - 1);  // O must be stable
-          if (!ok) break;
           tc::fence_after_sync();
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
+          for (int c = 0; c < 4 && ok; ++c) {
             uint32_t o[32];
-            tc::tmem_ld32(tm + COL_O + c * 32, o);
+            tc::tmem_ld32(tm + COL_O + half * 128 + c * 32, o);
             tc::tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tc::tmem_st32(tm + COL_O + c * 32, o);
+            tc::tmem_st32(tm + COL_O + half * 128 + c * 32, o);
           }
-          tc::tmem_wait_st();
         }
-        l += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
-        tc::tmem_st32(s_tm, pk[0]);
-        tc::tmem_st32(s_tm + 32, pk[1]);
+        l += ls;
+        tc::tmem_st32(s_tm, pk);  // each half over its own columns of S
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) {
+        if (lane == 0 && ok) {
           if (leader)
             mbar_arrive(&ctl->p_ready[jt & 1]);
           else
             pair::arrive_remote_tmem(p_ready_addr + (jt & 1) * 8);
         }
-        if (jt > 0) {
-          ok = pv_done(jt - 1);
-          if (!ok) break;
-        }
-        if (j == 0 && n > 0) put_out();
+        if (jt > 0) ok = ok && pv_done(jt - 1);
+        if (j == 0 && n > 0 && ok) put_out();
       }
+      if (left) break;
+      ok = vote64<true>(1 + wq, ok);  // the other half's maximum has been read
+      sc->part[half][row] = l;
+      ok = vote64<true>(1 + wq, ok);
       if (!ok) break;
       out_m = m_used;
-      out_l = l;
+      out_l = l + sc->part[half ^ 1][row];
       out_b = t.b;
       out_h = t.h;
       out_q0 = t.q0;
@@ -1096,7 +1144,7 @@ cudaError_t launch_stream(const CUtensorMap& mq, const CUtensorMap& mk, const CU
   const int64_t items = (int64_t)t.n_pairs * (t.head_pair ? t.Hq / 2 : t.Hq) * B;
   if (items > INT32_MAX - (1 << 20)) return cudaErrorInvalidValue;
   const int pairs = (int)std::min<int64_t>(items, multiprocessors() / 2);
-  return launch_early(k_prefill_stream, dim3(2 * pairs), 192, STREAM_SMEM, st, 0, mq, mk, mv, mo, t, (int)items);
+  return launch_early(k_prefill_stream, dim3(2 * pairs), STREAM_T, STREAM_SMEM, st, 0, mq, mk, mv, mo, t, (int)items);
 }
 
 }  // namespace

@@ -33,7 +33,8 @@ constexpr int PLAN_T = 1024;
 constexpr int SMALL_CTAS = 8;        // CTAs of a one-launch reserve
 constexpr int COPY_T = 256;
 constexpr int COPY_V = 4;            // 16-byte words per thread and tile
-constexpr int TILE_B = COPY_T * COPY_V * 16;
+// bytes that T threads copy at a time
+constexpr int tile_bytes(int T) { return T * COPY_V * 16; }
 
 struct Book {
   int32_t* table;
@@ -345,7 +346,7 @@ struct Seg {
   unsigned char* base;
   long long page_bytes;
   int head_bytes, row_bytes;
-  int tiles_per_head, tile0;  // tiles of TILE_B bytes; the segment's first tile of a page
+  int tiles_per_head, tile0;  // the segment's first tile of a page
 };
 
 struct CopyList {
@@ -385,11 +386,10 @@ __device__ __forceinline__ bool pair_ok(const CopyList& a, int k, int n) {
 }
 
 // CTA `cta` of `ctas` copies its share of the list's tiles, T threads of
-// COPY_V words each.
+// COPY_V words each (the list counts tiles of tile_bytes(T)).
 template <int T>
 __device__ __forceinline__ void copy_tiles(const CopyList& a, const Seg* seg, int cta, int ctas) {
-  constexpr int TILE = T * COPY_V * 16, PER = TILE / TILE_B;  // the list counts tiles of TILE_B bytes
-  static_assert(TILE % TILE_B == 0, "whole tiles");
+  constexpr int TILE = tile_bytes(T);
   const int n = a.n_dev ? *a.n_dev : a.n_host;
   int checked = -1;
   bool ok = true;
@@ -408,11 +408,10 @@ __device__ __forceinline__ void copy_tiles(const CopyList& a, const Seg* seg, in
     }
     const Seg& g = seg[lo];
     const int head = (t - g.tile0) / g.tiles_per_head, tile = (t - g.tile0) - head * g.tiles_per_head;
-    if (tile % PER) continue;
     const int rows = a.rows ? a.rows[(int64_t)k * a.stride] : a.ps;
-    const int bytes = min(rows * g.row_bytes - tile * TILE_B, TILE);
+    const int bytes = min(rows * g.row_bytes - tile * TILE, TILE);
     if (bytes <= 0) continue;
-    const int64_t at = (int64_t)head * g.head_bytes + (int64_t)tile * TILE_B;
+    const int64_t at = (int64_t)head * g.head_bytes + (int64_t)tile * TILE;
     const unsigned char* from = g.base + a.src[(int64_t)k * a.stride] * g.page_bytes + at;
     unsigned char* to = g.base + a.dst[(int64_t)k * a.stride] * g.page_bytes + at;
     uint4 v[COPY_V];
@@ -508,8 +507,8 @@ Book book_of(const gemma_page_book* b) {
   return Book{b->page_table, b->ref_count, b->n_seqs, b->pages_per_seq, b->n_pages, b->page_size};
 }
 
-// Segments of pools [i0, i0 + MAX_SEGS / 2) and their tiles.
-void segments(CopyList& a, Seg* seg, const gemma_page_pool* pools, int n_pools, int i0) {
+// Segments of pools [i0, i0 + MAX_SEGS / 2) and their tiles of `tile` bytes.
+void segments(CopyList& a, Seg* seg, const gemma_page_pool* pools, int n_pools, int i0, int tile) {
   a.n_segs = a.tiles = 0;
   for (int i = i0; i < std::min(n_pools, i0 + MAX_SEGS / 2); ++i) {
     const gemma_page_pool& p = pools[i];
@@ -524,7 +523,7 @@ void segments(CopyList& a, Seg* seg, const gemma_page_pool* pools, int n_pools, 
       const int heads = a.rows ? p.n_kv_heads : 1;
       g.row_bytes = a.rows ? row : row * p.n_kv_heads;
       g.head_bytes = a.ps * g.row_bytes;
-      g.tiles_per_head = (g.head_bytes + TILE_B - 1) / TILE_B;
+      g.tiles_per_head = (int)(((int64_t)g.head_bytes + tile - 1) / tile);
       g.tile0 = a.tiles;
       a.tiles += heads * g.tiles_per_head;
       seg[a.n_segs++] = g;
@@ -552,7 +551,7 @@ cudaError_t copy_pages(CopyList& list, const gemma_page_pool* pools, int n_pools
                        const int32_t* map, cudaStream_t st) {
   Seg seg[MAX_SEGS];
   for (int i0 = 0; i0 == 0 || i0 < n_pools; i0 += MAX_SEGS / 2) {
-    segments(list, seg, pools, n_pools, i0);
+    segments(list, seg, pools, n_pools, i0, tile_bytes(COPY_T));
     if (i0) map = nullptr;
     const int64_t names = map ? ((int64_t)bk.n_seqs * bk.pps + COPY_T - 1) / COPY_T : 0;
     const int64_t work = std::max(max_pairs * list.tiles, names);
@@ -657,14 +656,16 @@ int gemma_kv_pages_reserve(const gemma_page_book* book, const gemma_page_pool* p
   a.n_pages = book->n_pages;
   a.ps = book->page_size;
   a.status = status;
-  // One cluster copies about 0.4 MB a us, the whole GPU 3 MB, but in a second
-  // launch: up to 4 MB of tails (all rows splitting full pages) the cluster.
+  // The one-launch form saves a caller 2.4 us of CPU time a call; on the GPU it
+  // takes 1 us more with up to 1 MB of tails (all rows splitting full pages;
+  // half of it copied: 8.8 us against 7.8), 2.5 us more with 2 MB (10.6 against
+  // 8.1) and 10 with 8 MB. So: up to 1 MB.
   double most = 0.0;
   for (int i = 0; i < n_pools; ++i)
     most += (double)book->n_seqs * pools[i].n_kv_heads * book->page_size * pools[i].head_dim * 2;
-  if (n_pools > 0 && n_pools <= FEW_SEGS / 2 && most <= 4e6) {
+  if (n_pools > 0 && n_pools <= FEW_SEGS / 2 && most <= 1 << 20) {
     CopyArgs<FEW_SEGS> c;
-    segments(a, c.seg, pools, n_pools, 0);
+    segments(a, c.seg, pools, n_pools, 0, tile_bytes(PLAN_T));
     c.list = a;
     k_pages_reserve_small<FEW_SEGS><<<SMALL_CTAS, PLAN_T, 0, st>>>(book_of(book), seq_lens, new_tokens, lacking, plan, c);
     const cudaError_t es = cudaGetLastError();

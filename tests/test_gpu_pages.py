@@ -123,13 +123,19 @@ def reserve(dev, pools, lens, new):
     return lacking
 
 
+# few bytes at most (one launch): int8 with an odd number of 8-byte rows, runs of several tiles of a
+# CTA; many: a second launch copies
+SMALL, LARGE = (("int8", 1, 48), ("bf16", 1, 16)), (("bf16", 1, 256), ("int8", 3, 256), ("bf16", 2, 512))
+
+
+@pytest.mark.parametrize("kinds", [SMALL, (("bf16", 1, 320),), LARGE])
 @pytest.mark.parametrize("ps", [128, 256])
 @pytest.mark.parametrize("seed", range(4))
-def test_reserve_random(seed, ps):
+def test_reserve_random(seed, ps, kinds):
     rng = np.random.default_rng(100 + seed)
     n_seqs, pps, n_pages = 9, 8, 120
     bk = Book(n_seqs, pps, n_pages, ps)
-    dev, pools = on_device(bk), make_pools(n_pages, ps, seed)
+    dev, pools = on_device(bk), make_pools(n_pages, ps, seed, kinds)
     lens = [0] * n_seqs
     for step in range(6):
         new = [int(x) for x in rng.integers(0, ps + 40, n_seqs)]

@@ -807,18 +807,32 @@ cudaError_t launch_prefill_attn_tc(const PrefillAttnArgs& a, int B, int D, int k
 namespace {
 // CTAs per unit of rows and columns (the cluster) of the short-chunk form, 0
 // where the unsplit kernels are to be used: see launch_prefill_attn_rows.
+// Twice the CTAs pay while their clusters run at once (of 148 SMs 74 clusters of
+// 2, 33 of 4 and 15 of 8, as none crosses a GPC) and the key tiles that a CTA
+// saves (2.8 us each) take longer than the wider merge (4 us with all rows in
+// use). Measured (us, n = 1 being the unsplit kernels):
+//   8 q heads on 1, dim 512, window  512, 64 tokens: n = 1 21.5, 2 21.6, 4 20.9, 8 22.0
+//                                          5 tokens:      22.2,   18.4,   16.3,   16.0
+//                                        512 tokens:      26.1,   23.3,   41.9
+//   32 on 4,         dim 512, window 4096, 64 tokens:     81.3,   62.5,   46.0,   92.8
+//   32 on 16,        dim 256, window 1024, 64 tokens:     33.4,   31.5,   29.9,   50.4
+//                                        512 tokens:      41.4,   57.9
 template <int D>
 int rows_splits(const PrefillAttnArgs& a, int B) {
   using Cfg = TcCfg<D>;
   const int per_tile = BM / (a.Hq / a.Hkv);  // tokens per row tile
+  const int tokens = std::min(a.S, per_tile);
   const int64_t units = (int64_t)a.Hkv * Cfg::NV * B * ((a.S + per_tile - 1) / per_tile);
-  const int64_t tiles = std::min<int64_t>(((int64_t)a.window + a.S) / BN + 2 + (a.sinks + BN - 1) / BN,
+  const int64_t tiles = std::min<int64_t>(((int64_t)a.window + tokens) / BN + 2 + (a.sinks + BN - 1) / BN,
                                           (a.key_cap + BN - 1) / BN);
-  // clusters of n CTAs that have their SMs to themselves: 148 / n, and somewhat
-  // fewer as clusters do not cross GPCs (15 of 8, 33 of 4, 74 of 2)
-  const int64_t room = (int64_t)multiprocessors() * 17 / 20;
+  const int sms = multiprocessors();
+  const auto pays = [&](int n) {  // 2 n CTAs rather than n
+    const int64_t room = n == 1 ? sms : n == 2 ? sms * 9 / 10 : sms * 17 / 20;
+    const int64_t saved = (tiles + n - 1) / n - (tiles + 2 * n - 1) / (2 * n);
+    return units * 2 * n <= room && (double)saved * 2.8 > 4.0 * tokens / per_tile;
+  };
   int n = 1;
-  while (n < 8 && units * n * 2 <= room && n < tiles) n *= 2;
+  while (n < 8 && pays(n)) n *= 2;
   return n > 1 ? n : 0;
 }
 

@@ -506,10 +506,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
       tc::tmem_st32(s_tm, pk[0]);
       tc::tmem_st32(s_tm + 32, pk[1]);
       // consume P_{j-1} V_{j-1} before P_{j+1} V_{j+1} can complete the next
-      // phase of the same barrier (parity waits must not fall two behind). SK:
-      // after P_j is released, so that P_j V_j does not wait for the news of
-      // P_{j-1} V_{j-1} to come here and go back; P_j's arrival may then overtake
-      // the issuer's wait for P_{j-1}, hence a barrier per buffer of P
+      // phase of the same barrier (parity waits must not fall two behind). Not
+      // SK: P_j V_j need not wait for that news to come here and go back. S_j's
+      // commit, which this thread waited for, covers P_{j-2} V_{j-2} and all
+      // before it, so a wait for P_{j-1} V_{j-1} (above, and after the last tile)
+      // has one phase to wait for; and P_{j+2} is not released before S_{j+2},
+      // issued after P_j V_j, so a P-ready barrier per buffer of P is enough.
       if (!SK && j >= 1 && pv_seen < j) {
         if (!wait_all(&ctl->o_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, deadline, a.status, 46, j)) {
           ok = false;
@@ -527,13 +529,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
           mbar_arrive(&ctl->p_ready[SK ? j & 1 : 0]);
         else
           SK ? pair::arrive_remote_tmem(p_ready_addr + (j & 1) * 8) : pair::arrive_remote(p_ready_addr);
-      }
-      if (SK && j >= 1 && pv_seen < j) {
-        if (!wait_all(&ctl->o_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, deadline, a.status, 46, j)) {
-          ok = false;
-          break;
-        }
-        pv_seen = j;
       }
     }
     if (ok)
@@ -971,13 +966,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(STREAM_T, 1)
         a.lse[((int64_t)out_b * a.Hq + out_h) * a.S + out_q0 + row] =
             out_l > 0.f ? (out_m + __log2f(out_l)) * 0.69314718055994530942f : -INFINITY;
     };
-    // P V of key tile k is complete (each is waited for once, in order: parity
-    // waits must not fall two behind)
-    int pv_seen = 0;
     uint64_t deadline = 0;
+    // P V of the key tile before the current one is complete (all earlier ones are
+    // since S of the current one is, so there is one phase to wait for)
     const auto pv_done = [&](int k) -> bool {
-      if (pv_seen > k) return true;
-      pv_seen = k + 1;
       return wait_all(&ctl->o_done[k & 1], (k >> 1) & 1, abort_flag, deadline, a.status, 58, k, n);
     };
     const float factor = a.scale_log2;
@@ -1059,8 +1051,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(STREAM_T, 1)
           else
             pair::arrive_remote_tmem(p_ready_addr + (jt & 1) * 8);
         }
-        if (jt > 0) ok = ok && pv_done(jt - 1);
-        if (j == 0 && n > 0 && ok) put_out();
+        if (j == 0 && n > 0) {
+          ok = ok && pv_done(jt - 1);
+          if (ok) put_out();
+        }
       }
       if (left) break;
       ok = vote64<true>(1 + wq, ok);  // the other half's maximum has been read

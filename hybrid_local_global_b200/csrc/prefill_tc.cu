@@ -545,10 +545,12 @@ __global__ void __launch_bounds__(192, 1)
       tc::tmem_st32(s_tm, pk[0]);
       tc::tmem_st32(s_tm + 32, pk[1]);
       // consume P_{j-1} V_{j-1} before P_{j+1} V_{j+1} can complete the next
-      // phase of the same barrier (parity waits must not fall two behind). SK:
-      // after P_j is released, so that P_j V_j does not wait for the news of
-      // P_{j-1} V_{j-1} to come here and go back; P_j's arrival may then overtake
-      // the issuer's wait for P_{j-1}, hence a barrier per buffer of P
+      // phase of the same barrier (parity waits must not fall two behind). Not
+      // SK: P_j V_j need not wait for that news to come here and go back. S_j's
+      // commit, which this thread waited for, covers P_{j-2} V_{j-2} and all
+      // before it, so a wait for P_{j-1} V_{j-1} (above, and after the last tile)
+      // has one phase to wait for; and P_{j+2} is not released before S_{j+2},
+      // issued after P_j V_j, so a P-ready barrier per buffer of P is enough.
       if (!SK && j >= 1 && pv_seen < j) {
         if (!wait_all(&ctl->o_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, deadline, a.status, 16, j)) {
           ok = false;
@@ -559,13 +561,6 @@ __global__ void __launch_bounds__(192, 1)
       tc::tmem_wait_st();
       tc::fence_before_sync();
       mbar_arrive(&ctl->p_ready[SK ? j & 1 : 0]);
-      if (SK && j >= 1 && pv_seen < j) {
-        if (!wait_all(&ctl->o_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, deadline, a.status, 16, j)) {
-          ok = false;
-          break;
-        }
-        pv_seen = j;
-      }
     }
     if (ok && n_tiles > 0)
       ok = wait_all(&ctl->o_done[(n_tiles - 1) & 1], ((n_tiles - 1) >> 1) & 1, abort_flag, deadline,

@@ -1,8 +1,9 @@
 """Race check, on the CPU, of the barrier protocol of the window-plus-sinks
 prefill kernels, with the model of test_barrier_protocols_host.py.
 
-They release P_j to the issuer before they wait for P_{j-1} V_{j-1}, on one
-P-ready barrier per buffer of P. k_prefill_stream also walks several row tiles
+They wait for P_{j-1} V_{j-1} only where they need O (to rescale it, and for the
+output): S_j's commit covers P_{j-2} V_{j-2} and all before. There is one P-ready
+barrier per buffer of P. k_prefill_stream also walks several row tiles
 without a pause: Q is loaded again when the row tile's last S is done (q_empty),
 and the output of a row tile is taken out of TMEM after the first softmax of the
 next one, whose first P V waits for that (o_free). With one row tile the model
@@ -135,14 +136,9 @@ class Stream(Model):
         yield from pv(self.n - 1)
 
     def softmax(self, c):
-        seen = 0
-
         def pv_done(t, role):
-            nonlocal seen
-            if seen <= t:
-                seen = t + 1
-                while not self.check_wait(self.o_done[c][t & 1], t >> 1, role):
-                    yield
+            while not self.check_wait(self.o_done[c][t & 1], t >> 1, role):
+                yield
 
         def put_out(t):
             if t not in self.pv_done or self.writes(("O", c)):
@@ -168,9 +164,8 @@ class Stream(Model):
             self.p_written[c].add(j)
             (self.p_ready[j & 1] if self.per_buffer else self.p_ready[0]).arrive()
             yield
-            if j > 0:
-                yield from pv_done(j - 1, "pv_done")
             if j > 0 and j in self.first:
+                yield from pv_done(j - 1, "pv_done")
                 put_out(j - 1)
                 yield
         yield from pv_done(self.n - 1, "pv_done")

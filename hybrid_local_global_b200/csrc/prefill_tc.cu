@@ -818,7 +818,7 @@ int rows_splits(const PrefillAttnArgs& a, int B) {
   const int per_tile = BM / (a.Hq / a.Hkv);  // tokens per row tile
   const int tokens = std::min(a.S, per_tile);
   const int64_t units = (int64_t)a.Hkv * Cfg::NV * B * ((a.S + per_tile - 1) / per_tile);
-  const int64_t tiles = std::min<int64_t>(((int64_t)a.window + tokens) / BN + 2 + (a.sinks + BN - 1) / BN,
+  const int64_t tiles = std::min<int64_t>(((int64_t)a.window + tokens) / BN + 2 + ((int64_t)a.sinks + BN - 1) / BN,
                                           (a.key_cap + BN - 1) / BN);
   const int sms = multiprocessors();
   const auto pays = [&](int n) {  // 2 n CTAs rather than n

@@ -3,6 +3,9 @@ and generated tokens under a window plus sinks, with pages granted, forked,
 trimmed and compacted on the way; the whole step in a CUDA graph; calls on
 several streams; offsets past 32 bits."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -148,6 +151,85 @@ def test_captured_generation_step():
     ok()
     assert (out[2] == 0).all() and state[2].tolist() == [steps, 100 + steps, 0]
     assert (state[0].page_table >= 0).sum().item() <= 2 * 4
+
+
+FIRST_CALL = """
+import torch
+from hybrid_local_global_b200 import native
+torch.zeros(1, device="cuda")
+D, what = 256, %r
+bf = dict(dtype=torch.bfloat16, device="cuda")
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+q, k = torch.ones(1, 1, 4, D, **bf), torch.ones(1, 1, 2, D, **bf)
+out, pools = torch.zeros_like(q), [torch.zeros(4, 2, 128, D, **bf) for _ in range(2)]
+book = native.PageBook(1, 4, 4, 128, "cuda")
+book.page_table[0, 0], book.ref_count[0] = 0, 1
+lens, one, lacking = i32([1]), i32([1]), i32([0])
+POS = i32([[[0]]])
+ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+kw = dict(window=8, sinks=1, rope_frac=1.0, rope_theta=1e4, scale=0.1, workspace=ws)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    if what == "decode":
+        native.gemma_attn_decode_sinks(q[:, 0], k[:, 0], k[:, 0], *pools, book.page_table, seq_lens=one, max_seq_len=512,
+                                       out=out[:, 0], **kw)
+    elif what == "prefill":
+        native.gemma_attn_prefill_sinks(q, k, k, *pools, book.page_table, out=out, **kw)
+    elif what == "rope":
+        native.gemma_rope_axes(q, k, POS, axis_pairs=[16], rope_theta=1e4, q_out=out, k_out=k)
+    else:
+        native.gemma_kv_pages_reserve(book, pools, seq_lens=lens, new_tokens=one, lacking=lacking, workspace=ws)
+        native.gemma_kv_pages_compact(book, pools, n_live=lacking, workspace=ws)
+        out.fill_(1)
+g.replay()
+assert native.gemma_attn_sync_status() == 0
+assert (out == 1).all(), out
+"""
+
+
+@pytest.mark.parametrize("what", ["decode", "prefill", "rope", "pages"])
+def test_first_call_of_a_process_may_be_captured(what):
+    subprocess.run([sys.executable, "-c", FIRST_CALL % what], check=True, timeout=240,
+                   cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+
+def test_graphs_that_share_a_workspace_and_profiling():
+    """Two prompts' graphs on one workspace, replayed in turn; the same calls
+    with the library's launch events between the kernels."""
+    gen = synth.generator(12)
+    ws, jobs = torch.empty(64 << 20, dtype=torch.uint8, device=DEV), []
+    for D, Hq, Hkv, S in ((256, 16, 8, 700), (512, 8, 1, 60), (512, 16, 8, 300)):
+        pools = [torch.zeros(12, Hkv, 128, D, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        q, k, v = (synth.randn_bf16((1, S, h, D), gen).to(DEV) for h in (Hq, Hkv, Hkv))
+        out, table = torch.empty_like(q), torch.randperm(12)[None, :8].int().to(DEV)
+
+        def call(q=q, k=k, v=v, pools=pools, out=out, table=table, D=D):
+            native.gemma_attn_prefill_sinks(q, k, v, *pools, table, out=out, window=140, sinks=6, rope_frac=0.25,
+                                            rope_theta=1e6, scale=D ** -0.5, workspace=ws)
+
+        call()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+            call()
+        jobs.append((call, graph, out, out.clone()))
+    for _ in range(3):
+        for _, graph, out, _ in jobs:
+            out.zero_()
+            graph.replay()
+    ok()
+    for _, _, out, want in jobs:
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+    native.gemma_attn_profile(True)
+    try:
+        for call, _, out, want in jobs:
+            out.zero_()
+            call()
+            ok()
+            assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+    finally:
+        native.gemma_attn_profile(False)
 
 
 def test_calls_on_several_streams_at_once():

@@ -253,6 +253,14 @@ PREFILL += [
     dict(before=[0, 260], S=129, window=70, sinks=140, Hq=8, Hkv=8, D=512, ps=128),    # one head per CTA
     dict(before=[513, 100], S=200, window=128, sinks=1, Hq=16, Hkv=16, D=256, ps=256),
     dict(before=[90, 600], S=190, window=300, sinks=0, Hq=48, Hkv=16, D=256, ps=128),
+    # head_dim 256, several row tiles per CTA pair: pairs of heads, of row tiles (an odd number of
+    # them), few and many key tiles each
+    dict(before=[0, 130, 777], S=700, window=200, sinks=20, Hq=16, Hkv=8, D=256, ps=128),
+    dict(before=None, S=1300, window=1, sinks=0, Hq=16, Hkv=8, D=256, ps=128),
+    dict(before=[5, 300, 0, 128], S=600, window=130, sinks=140, Hq=9, Hkv=9, D=256, ps=256),
+    dict(before=[40, 3], S=300, window=90, sinks=3, Hq=40, Hkv=8, D=256, ps=128),
+    dict(before=[64, 700], S=300, window=256, sinks=33, Hq=16, Hkv=8, D=512, ps=128),
+    dict(before=[11], S=300, window=100, sinks=2, Hq=15, Hkv=5, D=512, ps=128),
 ]
 
 
@@ -300,6 +308,39 @@ def test_prefill_reports_pages_outside_the_pool():
                                         rope_theta=1e4, scale=0.1, out=torch.empty_like(q))
         assert native.gemma_attn_sync_status() == native.GEMMA_ERR_DEVICE_RANGE
         assert (pool == 0).all()
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,S", [(256, 16, 8, 700), (256, 2, 1, 40), (512, 16, 8, 300), (512, 5, 5, 500),
+                                        (256, 9, 9, 400)])
+def test_prefill_leaves_out_sequences_without_room(D, Hq, Hkv, S):
+    """Lengths that the table has no room for are reported; the others' rows
+    are what they are alone, and the outputs of the bad ones stay as they were."""
+    gen = synth.generator(41)
+    pps = (S + 200) // 128 + 1
+    q, k, v = (synth.randn_bf16((4, S, h, D), gen).to(DEV) for h in (Hq, Hkv, Hkv))
+    kw = dict(window=150, sinks=5, rope_frac=0.25, rope_theta=1e6, scale=D ** -0.5)
+    table = torch.arange(4 * pps, dtype=torch.int32, device=DEV).view(4, pps)
+
+    def run(lens):
+        pools = [torch.zeros(4 * pps, Hkv, 128, D, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        out = torch.full_like(q, 7.0)
+        native.gemma_attn_prefill_sinks(q, k, v, *pools, table, out=out,
+                                        seq_lens_before=torch.tensor(lens, dtype=torch.int32, device=DEV), **kw)
+        return out, pools, native.gemma_attn_sync_status()
+
+    good, pa, status = run([3, 0, 100, 1])
+    assert status == 0
+    some, pb, status = run([3, -1, 100, pps * 128 - S + 1])
+    assert status == native.GEMMA_ERR_DEVICE_RANGE
+    for b in (0, 2):
+        assert same_bits(some[b], good[b])
+    for b in (1, 3):
+        assert (some[b] == 7).all() and all((p[b * pps:(b + 1) * pps] == 0).all() for p in pb)
+    none, pc, status = run([-1, -5, 1 << 30, pps * 128])
+    assert status == native.GEMMA_ERR_DEVICE_RANGE
+    assert (none == 7).all() and all((p == 0).all() for p in pc)
+    again, pd, status = run([3, 0, 100, 1])
+    assert status == 0 and same_bits(again, good)
 
 
 def test_chunks_and_steps_agree():

@@ -1185,9 +1185,10 @@ int gemma_attn_prefill_sinks(const void* q, const void* k_new, const void* v_new
   {
     ProfScope p_attn(GEMMA_KERNEL_PREFILL_ATTN, st);
     const int splits = prefill_rows_splits(aa, batch, head_dim);
-    e = splits ? launch_prefill_attn_rows(aa, batch, head_dim, splits, st)
-        : even || head_dim == 256 ? launch_prefill_attn_pair(aa, batch, head_dim, page_size, 0, even, st)
-                                  : launch_prefill_attn_tc(aa, batch, head_dim, page_size, 0, st);
+    e = splits            ? launch_prefill_attn_rows(aa, batch, head_dim, splits, st)
+        : head_dim == 256 ? launch_prefill_attn_stream(aa, batch, even, st)
+        : even            ? launch_prefill_attn_pair(aa, batch, head_dim, page_size, 0, 1, st)
+                          : launch_prefill_attn_tc(aa, batch, head_dim, page_size, 0, st);
     p_attn.done();
   }
   if (e != cudaSuccess) return cuda_fail(e, "prefill attention launch");

@@ -229,6 +229,7 @@ int prefill_rows_splits(const PrefillAttnArgs& a, int B, int D);
 cudaError_t launch_prefill_attn_rows(const PrefillAttnArgs& a, int B, int D, int n, cudaStream_t st);
 // head_pair: the pair takes two q heads of one KV head on the same query
 // tile (used when q heads per KV head is even) instead of two query tiles.
+cudaError_t launch_prefill_attn_stream(const PrefillAttnArgs& a, int B, int head_pair, cudaStream_t st);
 cudaError_t launch_prefill_attn_pair(const PrefillAttnArgs& a, int B, int D, int key_rows_total,
                                      int kv_token_major, int head_pair, cudaStream_t st);
 // Single-token decode with window and sinks on a paged cache, one launch

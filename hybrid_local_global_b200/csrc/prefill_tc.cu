@@ -779,7 +779,7 @@ cudaError_t launch_prefill_attn_tc(const PrefillAttnArgs& a, int B, int D, int k
   t.n_qtiles = (a.S + BM - 1) / BM;
   if (D == 256) {
     using Cfg = TcCfg<256>;
-    if (a.sinks >= 0) return cudaErrorInvalidValue;  // launch_prefill_attn_pair's
+    if (a.sinks >= 0) return cudaErrorInvalidValue;  // launch_prefill_attn_stream's
     auto kern = k_prefill_tc<256, false, false>;
     cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);

@@ -442,8 +442,10 @@ EXPORTED += ["gemma_attn_prefill_sinks", "gemma_attn_decode_sinks_workspace_size
 
 
 # These calls may be issued every few microseconds, so their checks use the
-# cheap accessors: get_device() for tensors, the raw current stream.
+# cheap accessors: get_device() for tensors, the raw current stream and device
+# (a CUDA tensor has been seen, so CUDA is initialised).
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _on(index, stream, what, call, *args):
@@ -457,7 +459,7 @@ def _on(index, stream, what, call, *args):
         raw = stream.cuda_stream
     else:
         raise ValueError("%s: stream of %s, tensors on cuda:%d" % (what, stream.device, index))
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         return _check(call(*args, raw))
     with torch.cuda.device(index):
         return _check(call(*args, raw))
@@ -504,10 +506,13 @@ def _sinks_args(q, k_new, v_new, k_pool, v_pool, page_table, out, lens, lens_nam
 def _workspace(workspace, size, index):
     """(pointer, bytes) of the caller's workspace, or of one of size() bytes."""
     if workspace is None:
-        workspace = torch.empty(max(size(), 1), dtype=torch.uint8, device="cuda:%d" % index)
+        n = size()
+        if n == 0:
+            return None, None, 0
+        workspace = torch.empty(n, dtype=torch.uint8, device="cuda:%d" % index)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous tensor on device %d" % index)
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.nbytes
 
 
 def gemma_attn_prefill_sinks(q, k_new, v_new, k_pool, v_pool, page_table, *, window, sinks, rope_frac, rope_theta,
@@ -645,18 +650,17 @@ def gemma_kv_pages_copy(pools, *, src, dst, stream=None):
                src.shape[0])
 
 
-def _token_stride(t, name, tokens, D, index):
-    """Elements between tokens of a bf16 tensor [..., heads, D] of this token
-    shape, whose heads are dense and whose tokens are evenly spaced."""
-    shape = t.shape
+def _token_stride(t, name, index):
+    """Elements between tokens of a bf16 tensor [..., heads, D] on this device,
+    whose heads are dense and whose tokens are evenly spaced."""
     if t.dtype is not _BF16 or t.get_device() != index:
         raise TypeError("%s must be a bf16 tensor on device %d" % (name, index))
-    if shape[:-2] != tokens or shape[-1] != D:
-        raise ValueError("%s has shape %s: tokens %s and head_dim %d expected" % (name, tuple(shape), tuple(tokens), D))
+    shape = t.shape
+    D = shape[-1]
     if t.is_contiguous():
         return shape[-2] * D
     stride = t.stride()
-    lead = [(n, s) for n, s in zip(tokens, stride) if n != 1]
+    lead = [(n, s) for n, s in zip(shape[:-2], stride) if n != 1]
     if stride[-1] != 1 or (shape[-2] != 1 and stride[-2] != D) or any(
             s0 != n1 * s1 for (_, s0), (n1, s1) in zip(lead, lead[1:])):
         raise ValueError("%s: heads must be dense and tokens evenly spaced" % name)
@@ -668,22 +672,27 @@ def gemma_rope_axes(q, k, positions, *, axis_pairs, rope_theta, q_out, k_out=Non
     (or None) turned by positions int32 [n_axes, ...] into q_out and k_out
     (which may be q and k). Tokens may be strided, e.g. slices of a fused
     projection; see GEMMA_ROPE_* for flags."""
-    if q.dim() < 3:
+    shape = q.shape
+    if len(shape) < 3:
         raise ValueError("q must be [..., heads, head_dim]")
     i = q.get_device()
-    lead, Hq, D = q.shape[:-2], q.shape[-2], q.shape[-1]
-    if q_out.shape != q.shape:
+    *lead, Hq, D = shape
+    if q_out.shape != shape:
         raise ValueError("q_out must have the shape of q")
-    qs, qos = _token_stride(q, "q", lead, D, i), _token_stride(q_out, "q_out", lead, D, i)
+    qs, qos = _token_stride(q, "q", i), _token_stride(q_out, "q_out", i)
     ks = kos = Hkv = 0
     k_p = ko_p = None
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out go together")
     if k is not None:
-        if k_out.shape != k.shape:
+        k_shape = k.shape
+        *k_lead, Hkv, k_D = k_shape
+        if k_lead != lead or k_D != D:
+            raise ValueError("k has shape %s: tokens %s and head_dim %d expected" % (tuple(k_shape), tuple(lead), D))
+        if k_out.shape != k_shape:
             raise ValueError("k_out must have the shape of k")
-        ks, kos = _token_stride(k, "k", lead, D, i), _token_stride(k_out, "k_out", lead, D, i)
-        Hkv, k_p, ko_p = k.shape[-2], k.data_ptr(), k_out.data_ptr()
+        ks, kos = _token_stride(k, "k", i), _token_stride(k_out, "k_out", i)
+        k_p, ko_p = k.data_ptr(), k_out.data_ptr()
     n_axes = len(axis_pairs)
     pos = _need(positions, "positions", _I32, (n_axes, *lead), i)
     return _on(i, stream, "gemma_rope_axes", _rope_axes, q.data_ptr(), qs, k_p, ks, pos, n_axes,

@@ -534,7 +534,8 @@ __global__ void __launch_bounds__(NT, CTAS)
 #pragma unroll
         for (int n = 0; n < 8; ++n)
           v[n] = seen ? (__uint_as_float(r[n]) + __uint_as_float(r[n + 8])) * a.scale_log2 : -INFINITY;
-        if (own_new && p0 + kl == len_c) {
+        // (its row is in the last tile; an earlier one of few blocks may end less than 128 before it)
+        if (own_new && j == n_tiles - 1 && p0 + kl == len_c) {
           // head n's dims lie in the warps with threads of row n: D / 256 of them
 #pragma unroll
           for (int n = 0; n < 8; ++n)

@@ -131,6 +131,15 @@ def test_decode_every_split_count(B, Hkv, window):
     run_decode(lens=lens, window=window, sinks=40, Hq=2 * Hkv, Hkv=Hkv, D=512, ps=128)
 
 
+@pytest.mark.parametrize("window", [14, 33, 60, 100, 127])
+@pytest.mark.parametrize("sinks,D,Hkv,B", [(0, 512, 1, 1), (0, 256, 2, 2), (9, 256, 2, 3), (9, 256, 16, 24), (0, 512, 4, 80)])
+def test_decode_small_window_across_a_tile_boundary(window, sinks, D, Hkv, B):
+    """The window begins in one tile and ends in the next, less than 128
+    positions on, in one CTA (many sequences) or two."""
+    lens = [(134, 777, 129, 256 + window // 2, 391, 640 + window - 1)[b % 6] + 128 * (b // 6) for b in range(B)]
+    run_decode(lens=lens, window=window, sinks=sinks, Hq=2 * Hkv, Hkv=Hkv, D=D, ps=128)
+
+
 def test_decode_equals_global_paged_decode_when_everything_is_visible():
     lens, Hq, Hkv, D, ps = [700, 31], 8, 1, 512, 128
     held = [list(range(6)), [0]]

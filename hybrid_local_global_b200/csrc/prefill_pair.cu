@@ -35,7 +35,8 @@
 //
 // V rows past the sequence end must be finite (their P is 0, but 0 * inf is
 // nan): on the one key tile that crosses the end, the MMA warp clears those
-// rows in both CTAs' stages before the P.V product.
+// rows in both CTAs' stages before the P.V product (SK: and those of the edge
+// tiles that no row of the pair sees, tc::SeenRows).
 //
 // Every wait is bounded by a %globaltimer deadline. On a timeout the CTA
 // raises its abort flag and records GEMMA_ERR_DEVICE_TIMEOUT; the leader
@@ -260,16 +261,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
             break;
           }
           taken = item + 1;
-          const int64_t rows_valid = n_keys - tile_key(j - 1);
-          if (rows_valid < BN) {
-            clear_v_tail_pair(sStage + s * STAGE_B, rows_valid > 0 ? (int)rows_valid : 0, lane);
-            __syncwarp();
-          }
-          tc::fence_after_sync();
-#pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)
+          const int64_t v_key = tile_key(j - 1);
+          const auto product = [&](int kk, bool add) {
             pair::mma2_ts_if(go, tmem + COL_O, p_tm + kk * 8, dv + (uint64_t)((s * STAGE_B + kk * 2048) >> 4), IDESC_PV,
-                             (j - 1 > 0 || kk) ? 1u : 0u);
+                             add ? 1u : 0u);
+          };
+          const tc::SeenRows seen =
+              SK ? tc::seen_rows(j - 1 < n_st, a.sinks - v_key, lo_first - v_key, hi_last + 1 - v_key)
+                 : tc::seen_rows(false, 0, 0, n_keys - v_key);
+          if (SK && !seen.all()) {
+            if (seen.gap0 < seen.gap1) clear_v_rows_pair(sStage + s * STAGE_B, seen.gap0, seen.gap1, lane);
+            if (seen.tail < seen.k1 * 16) clear_v_rows_pair(sStage + s * STAGE_B, seen.tail, seen.k1 * 16, lane);
+            __syncwarp();
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int kk = seen.k0; kk < seen.k1; ++kk) product(kk, j - 1 > 0 || kk > seen.k0);
+          } else {
+            if (!SK && seen.tail < BN) {
+              clear_v_rows_pair(sStage + s * STAGE_B, seen.tail, BN, lane);
+              __syncwarp();
+            }
+            tc::fence_after_sync();
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk) product(kk, j - 1 > 0 || kk);
+          }
           pair::commit2_mc_if(go, smem_u32(&ctl->empty[s]), BOTH);
           pair::commit2_mc_if(go, smem_u32(&ctl->o_done[(j - 1) & 1]), BOTH);
           ++item;

@@ -108,13 +108,13 @@ __device__ __forceinline__ float max_row(const uint32_t (&r)[4][32]) {
   return max8(mx);
 }
 
-// Zero V rows [r0, BN) of a stage (the whole warp): both 64-column boxes, in this CTA (local
+// Zero V rows [r0, r1) of a stage (the whole warp): both 64-column boxes, in this CTA (local
 // stores) and in the peer (distributed shared memory), then make the writes
 // visible to the tensor core's reads.
-__device__ __forceinline__ void clear_v_tail_pair(uint32_t stage, int r0, int lane) {
+__device__ __forceinline__ void clear_v_rows_pair(uint32_t stage, int r0, int r1, int lane) {
   const uint32_t peer = pair::map_to(stage, 1);
   const uint32_t self = pair::map_to(stage, 0);
-  for (int i = lane; i < (BN - r0) * 16; i += 32) {
+  for (int i = lane; i < (r1 - r0) * 16; i += 32) {
     const uint32_t off = (uint32_t)(((i >> 3) & 1) * CHUNK_V + (r0 + (i >> 4)) * 128 + (i & 7) * 16);
     asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(self + off), "r"(0) : "memory");
     asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(peer + off), "r"(0) : "memory");

@@ -54,6 +54,7 @@ struct RowTile {
   int b, h, g, q0;  // this CTA's
   int n_tiles, n_st;
   int pos0, n_keys, kt0;
+  int lo, end;  // keys that the rows see, sinks apart
   __device__ __forceinline__ int key(int j) const { return (j < n_st ? j : kt0 + j - n_st) * BN; }
 };
 
@@ -75,6 +76,8 @@ __device__ __forceinline__ bool row_tile(const PairArgs& a, int i, int rank, Row
   t->pos0 = (int)pos0;
   t->n_keys = (int)n_keys;
   t->kt0 = (int)(lo_first / BN);
+  t->lo = (int)lo_first;
+  t->end = (int)hi_last + 1;
   t->n_st = (int)min(((int64_t)a.sinks + BN - 1) / BN, (int64_t)t->kt0);
   t->n_tiles = (int)(hi_last / BN) - t->kt0 + 1 + t->n_st;
   return true;
@@ -260,7 +263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(STREAM_T, 1)
       const uint64_t dk = tc::smem_desc_sw128(sStage, 16, 1024), dv = tc::smem_desc_sw128(sStage, CHUNK_V, 1024);
       int item = 0, taken = 0;
       uint64_t deadline = 0;
-      int v_rows = 0;       // valid rows of the key tile before,
+      tc::SeenRows seen{};  // rows of the key tile before,
       bool v_first = true;  // the first of its row tile,
       int v_n = 0;          // number v_n
       const auto pv = [&](int k) -> bool {  // O (+)= P_k V_k
@@ -274,16 +277,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(STREAM_T, 1)
         const int s = item % NSTAGE;
         if (!wait_all(&ctl->full[s], (item / NSTAGE) & 1, abort_flag, deadline, a.status, 55, item, s, k)) return false;
         taken = ++item;
-        if (v_rows < BN) {
-          clear_v_tail_pair(sStage + s * STAGE_B, v_rows > 0 ? v_rows : 0, lane);
-          __syncwarp();
-        }
-        tc::fence_after_sync();
         const uint32_t p_tm = tmem + COL_S + (uint32_t)(k & 1) * 128;
-#pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
+        const auto product = [&](int kk, bool add) {
           pair::mma2_ts_if(go, tmem + COL_O, p_tm + (kk >> 2) * 64 + (kk & 3) * 8,
-                           dv + (uint64_t)((s * STAGE_B + kk * 2048) >> 4), IDESC_PV, (!v_first || kk) ? 1u : 0u);
+                           dv + (uint64_t)((s * STAGE_B + kk * 2048) >> 4), IDESC_PV, add ? 1u : 0u);
+        };
+        if (seen.all()) {
+          tc::fence_after_sync();
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk) product(kk, !v_first || kk);
+        } else {
+          if (seen.gap0 < seen.gap1) clear_v_rows_pair(sStage + s * STAGE_B, seen.gap0, seen.gap1, lane);
+          if (seen.tail < seen.k1 * 16) clear_v_rows_pair(sStage + s * STAGE_B, seen.tail, seen.k1 * 16, lane);
+          __syncwarp();
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int kk = seen.k0; kk < seen.k1; ++kk) product(kk, !v_first || kk > seen.k0);
+        }
         pair::commit2_mc_if(go, smem_u32(&ctl->empty[s]), BOTH);
         pair::commit2_mc_if(go, smem_u32(&ctl->o_done[k & 1]), BOTH);
         return true;
@@ -313,7 +323,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(STREAM_T, 1)
           pair::commit2_mc_if(go, smem_u32(&ctl->s_full[jt & 1]), BOTH);
           if (j == t.n_tiles - 1) pair::commit2_mc_if(go, smem_u32(&sc->q_empty), BOTH);
           if (jt > 0) ok = pv(jt - 1);
-          v_rows = t.n_keys - t.key(j);
+          seen = tc::seen_rows(j < t.n_st, (int64_t)a.sinks - t.key(j), t.lo - t.key(j), t.end - t.key(j));
           v_first = j == 0;
           v_n = n;
         }

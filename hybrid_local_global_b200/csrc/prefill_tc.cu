@@ -200,6 +200,7 @@ __global__ void __launch_bounds__(192, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   int64_t pos0, n_keys, kt0;
+  int64_t v_lo = 0, v_end = 0;  // SK: keys that the rows see, sinks apart
   int n_tiles;
   int n_st = 0;  // SK: tiles of the sinks, before tile kt0
   int j0 = 0;    // ROWS: this CTA's first tile
@@ -231,6 +232,8 @@ __global__ void __launch_bounds__(192, 1)
     kt0 = lo_first / BN;
     n_tiles = (int)(hi_last / BN - kt0 + 1);
     if (SK) {
+      v_lo = lo_first;
+      v_end = hi_last + 1;
       const int64_t sink_tiles = ((int64_t)a.sinks + BN - 1) / BN;
       n_st = (int)(sink_tiles < kt0 ? sink_tiles : kt0);
       n_tiles += n_st;
@@ -390,6 +393,8 @@ __global__ void __launch_bounds__(192, 1)
           break;
         }
         const int64_t tile_key0 = tile_key(j - 1);
+        const tc::SeenRows seen = tc::seen_rows(SK && j - 1 + j0 < n_st, SK ? a.sinks - tile_key0 : 0,
+                                                SK ? v_lo - tile_key0 : 0, (SK ? v_end : n_keys) - tile_key0);
         const uint32_t p_tm = tmem + COL_S + (uint32_t)((j - 1) & 1) * 128;
         for (int half = 0; half < 2; ++half, ++item) {
           const int s = item % NSTAGE;
@@ -399,23 +404,35 @@ __global__ void __launch_bounds__(192, 1)
           }
           taken = item + 1;
           const uint32_t st = sStage + s * STAGE_B;
-          const int64_t rows_valid = n_keys - (tile_key0 + half * 64);
-          if (rows_valid < 64) {
-            // keys past the sequence: their P is 0, but their V rows must be finite
-            const int r0 = rows_valid > 0 ? (int)rows_valid : 0;
-            for (int idx = lane; idx < (64 - r0) * 4 * 8; idx += 32) {
+          const auto clear = [&](int from, int to) {  // rows of the tile, of which 64 lie in this stage
+            const int r0 = max(from - half * 64, 0), r1 = min(to - half * 64, 64);
+            if (r0 >= r1) return;
+            for (int idx = lane; idx < (r1 - r0) * 4 * 8; idx += 32) {
               const int r = r0 + idx / 32, c = (idx / 8) % 4, u = idx % 8;
               *reinterpret_cast<uint4*>(sm + (st - base) + c * 8192 + r * 128 + u * 16) =
                   make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
-          }
-          tc::fence_after_sync();
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
+          };
+          const auto product = [&](int kk, bool add) {
             tc::mma_ts_if(go, tmem + COL_O, p_tm + half * 32 + kk * 8,
-                          dv + (uint64_t)((s * STAGE_B + kk * 2048) >> 4), IDESC_PV, (j - 1 > 0 || half || kk) ? 1u : 0u);
+                          dv + (uint64_t)((s * STAGE_B + kk * 2048) >> 4), IDESC_PV, add ? 1u : 0u);
+          };
+          if (SK && !seen.all()) {
+            clear(seen.gap0, seen.gap1);
+            clear(seen.tail, seen.k1 * 16);
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int kk = max(seen.k0 - half * 4, 0); kk < min(seen.k1 - half * 4, 4); ++kk)
+              product(kk, j - 1 > 0 || half * 4 + kk > seen.k0);
+          } else {
+            // keys past the sequence: their P is 0, but their V rows must be finite
+            if (!SK) clear(seen.tail, BN);
+            tc::fence_after_sync();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) product(kk, j - 1 > 0 || half || kk);
+          }
           tc::commit_if(go, smem_u32(&ctl->empty[s]));
         }
         if (!ok) break;

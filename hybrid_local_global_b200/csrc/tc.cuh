@@ -203,5 +203,27 @@ __device__ __forceinline__ uint32_t visible_bits(int c0, int lo, int hi, int sin
   return (from | sinks) & upto;
 }
 
+// Which of a V tile's 128 rows any query row of a row tile sees: all but
+// [gap0, gap1) and those from `tail` on. The products run over the groups of 16
+// rows [k0, k1) that hold such a row; unseen rows among those are cleared first,
+// as their weight is 0, but 0 * NaN is not. Arguments relative to the tile: where
+// the sinks, the first row's window and the last row's keys end, begin and end.
+struct SeenRows {
+  int gap0, gap1, tail, k0, k1;
+  __device__ __forceinline__ bool all() const { return k0 == 0 && k1 == 8 && gap0 >= gap1 && tail == 128; }
+};
+__device__ __forceinline__ SeenRows seen_rows(bool sink_tile, int64_t sinks, int64_t lo, int64_t end) {
+  const auto clamp = [](int64_t x) { return (int)(x < 0 ? 0 : x > 128 ? 128 : x); };
+  SeenRows s;
+  s.gap0 = clamp(sinks);
+  s.gap1 = sink_tile ? 128 : clamp(lo);
+  s.tail = sink_tile ? 128 : clamp(end);
+  s.k0 = s.gap0 > 0 ? 0 : s.gap1 / 16;
+  s.k1 = ((sink_tile ? s.gap0 : s.tail) + 15) / 16;
+  s.gap0 = max(s.gap0, s.k0 * 16);
+  s.gap1 = min(s.gap1, s.k1 * 16);
+  return s;
+}
+
 }  // namespace tc
 }  // namespace hlg

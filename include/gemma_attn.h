@@ -332,8 +332,7 @@ int gemma_attn_decode_multi_paged(const void* q, const void* k_new, const void* 
 /*        nothing is written for it and it is no error. A length below 0 or */
 /*        above max_seq_len gives zeros and GEMMA_ERR_DEVICE_RANGE.          */
 /* Values at positions that no query of the call sees are not used, what-   */
-/* ever they hold, with one exception: in prefill a position that shares a  */
-/* 128-position block with a visible one must hold finite values.            */
+/* ever they hold.                                                          */
 /* flags: GEMMA_F_SHARED, GEMMA_F_KEQV. bf16 pools only (GEMMA_F_KV_INT8:   */
 /*        GEMMA_ERR_UNSUPPORTED). No two sequences of a call may write the  */
 /*        same page (gemma_kv_pages_reserve sees to that).                   */

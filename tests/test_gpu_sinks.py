@@ -217,7 +217,6 @@ def run_prefill(before, S, window, sinks, Hq, Hkv, D, ps, seed=21, keqv=False, s
     B, pps = len(lens), (max(lens) + S) // ps + 2
     held = [sorted(kept_pages(n, window, sinks, ps) | set(range(n // ps, (n + S - 1) // ps + 1))) for n in lens]
     cached = [n + S if shared else n for n in lens]
-    # cached rows are finite (a prefill asks that of a visible position's 128-block)
     K, V, kp, vp, table = make_cache(cached, held, Hkv, D, ps, pps, seed, keqv)
     gen = synth.generator(seed + 1)
     q = synth.randn_bf16((B, S, Hq, D), gen)

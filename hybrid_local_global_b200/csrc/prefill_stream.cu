@@ -14,10 +14,10 @@
 // a key tile took 3650 cycles, of which the softmax 2650; with two 2600, of
 // which 1024 are its exponentials at the special-function rate and the products
 // 2048. B1 S8191 Hq32 Hkv16, window 1024, 16 sinks: 355 us with one CTA per row
-// tile, 239 so (1400 TFLOP/s counting the masked parts of edge tiles), the
+// tile, 247 so (1390 TFLOP/s counting the masked parts of edge tiles), the
 // rotation before it another 97.
 //
-// Waits, timeouts and the clearing of V's tail are k_prefill_pair's.
+// Waits, timeouts and the clearing of V's unseen rows are k_prefill_pair's.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

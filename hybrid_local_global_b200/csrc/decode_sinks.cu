@@ -669,7 +669,10 @@ __global__ void __launch_bounds__(NT, CTAS)
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, C::TMEM_COLS);
   }
-  // weight of each split's share, 2^(m_s - M) / L (thread: head tid % 8 of split tid / 8)
+  // Weight of each split's share, 2^(m_s - M) / L (thread: head tid % 8 of split
+  // tid / 8). A head's maximum is -inf in a split that saw no number above it: no
+  // tile at all (sum 0), logits of -inf (0) or only NaN (a NaN sum, which must reach
+  // L: the softmax of NaN is NaN, and so is 0 / 0 where every logit is -inf).
   if (tid < n_splits * 8) {
     const int n = tid & 7;
     float M = -INFINITY, L = 0.f;
@@ -678,23 +681,22 @@ __global__ void __launch_bounds__(NT, CTAS)
     for (int s = 0; s < n_splits; ++s) {
       const float2 ml = ctl->ml[s][n];
       ok = ok && !(ml.y < 0.f);
-      if (ml.x != -INFINITY) L += tc::ex2(ml.x - M) * ml.y;
+      L += (ml.x == -INFINITY ? 0.f : tc::ex2(ml.x - M)) * ml.y;
     }
     const float m = ctl->ml[tid >> 3][n].x;
-    ctl->wgt[tid >> 3][n] = m == -INFINITY ? 0.f : tc::ex2(m - M) / L;
+    ctl->wgt[tid >> 3][n] = (m == -INFINITY ? 0.f : tc::ex2(m - M)) / L;
     if (!ok) ctl->abort = 1;  // some CTA gave up: no output
   }
   __syncthreads();
   if (*abort_flag) return;
+  const int n_full = (sp.tiles + per - 1) / per;  // splits with tiles: the others pushed no share
   for (int i = tid; i < 2 * cols; i += NT) {  // (heads 4 hh .. 4 hh + 3, column d)
     const int hh = i >> log_cols, d = i & (cols - 1);
     if (4 * hh >= G) break;
     float x[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < n_splits; ++s) {
+    for (int s = 0; s < n_full; ++s) {
       const float4 w = *reinterpret_cast<const float4*>(&ctl->wgt[s][4 * hh]);
       const float4 v = *reinterpret_cast<const float4*>(sm + C::MERGE_OFF + ((s << log_cols) + d) * 32 + hh * 16);
-      // a split without keys pushed nothing
-      if (ctl->ml[s][4 * hh].x == -INFINITY) continue;
       x[0] += w.x * v.x;
       x[1] += w.y * v.y;
       x[2] += w.z * v.z;

@@ -25,11 +25,17 @@ def cache(B, pps, Hkv, D, seed):
     return pools, table
 
 
-def check(got, clean, hit):
-    """hit: mask of the rows [..., heads] that must be NaN; the others as in `clean`."""
+def check(got, clean, hit, v_absmax=None):
+    """hit: mask of the rows [..., heads] that must be NaN; the others as in
+    `clean`, bit for bit, or (v_absmax given) as close as 32-bit sums taken
+    against another running maximum come."""
     assert torch.isfinite(clean).all()
     assert torch.isnan(got[hit]).all(), torch.nonzero(~torch.isnan(got).all(-1) & hit)[:4].tolist()
-    assert torch.equal(bits(got[~hit]), bits(clean[~hit]))
+    a, b = got[~hit], clean[~hit]
+    if v_absmax is None:
+        assert torch.equal(bits(a), bits(b))
+    else:
+        assert ((a.double() - b.double()).abs() <= 2.0 ** -7 * b.double().abs() + 2.0 ** -13 * v_absmax).all()
 
 
 # sequences, q heads, KV heads, dim, window: clusters of several CTAs and single ones, groups of 1 to 8
@@ -64,7 +70,12 @@ def test_decode_query(case, bad):
         x, hit = q.clone(), torch.zeros(B, Hq, dtype=torch.bool, device=DEV)
         x[B // 2, heads, D - 1] = bad
         hit[B // 2, heads] = True
-        check(run(x, pools), clean, hit)
+        # The new token's logit is then infinite, so the heads' running maxima move at that tile
+        # where they would have stayed (by less than 2^8): the others' weights are formed against
+        # another power of two. A weight is held as two bf16, off by 2^-8 of 2^-8 of itself: an
+        # output differs by at most 2 * 2^-16 max|v| before its rounding (2^-13 covers the 32-bit
+        # sums too), which may then fall to the next bf16, 2^-7 of it away.
+        check(run(x, pools), clean, hit, None if math.isnan(bad) else float(pools[1].abs().max()))
 
 
 @pytest.mark.parametrize("rows", ["one", "tile", "all"])
@@ -83,5 +94,5 @@ def test_decode_keys(case, rows):
     for j in spots:
         k[table[b, j // 128], g, j % 128, 3] = math.nan
     hit = torch.zeros(B, Hq, dtype=torch.bool, device=DEV)
-    hit[b, g * (Hq // Hkv):(g + 1) * (Hq // Hkv)] = True
+    hit[b, g * (Hq // Hkv):(g + 1) * (Hq // Hkv)] = any(j >= n - window for j in spots)  # some key that is seen
     check(run(q, [k, pools[1]]), clean, hit)

@@ -571,6 +571,14 @@ size_t plan_bytes(int64_t n_seqs, int64_t pps, int64_t n_pages) {
   return 256 + std::max(reserve, compact);
 }
 
+// Lets a kernel have as much dynamic shared memory as its largest book asks for:
+// the same on every call, so that no thread with a small book lowers what
+// another's launch counts on, and no threshold depends on what the kernel declares.
+template <class... P>
+cudaError_t allow_shared(void (*kern)(P...), int bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 int check_plan_ws(const gemma_page_book* b, const void* ws, size_t bytes) {
   if (!ws || bytes < plan_bytes(b->n_seqs, b->pages_per_seq, b->n_pages))
     return err(GEMMA_ERR_CAPACITY, "workspace smaller than gemma_kv_pages_workspace_size");
@@ -597,8 +605,7 @@ int gemma_kv_pages_fork(const gemma_page_book* book, const int32_t* parents, voi
   int* status = device_status();
   if (!status) return err(GEMMA_ERR_CUDA, "no CUDA device");
   const int smem = book->n_seqs * FORK_C * 4;
-  cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024) e = cudaFuncSetAttribute(k_pages_fork, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_shared(k_pages_fork, MAX_SEQS * FORK_C * 4);
   if (e != cudaSuccess) return cuda_err(e, "page fork");
   k_pages_fork<<<(book->pages_per_seq + FORK_C - 1) / FORK_C, 256, smem, static_cast<cudaStream_t>(stream)>>>(
       book_of(book), parents, status);
@@ -708,8 +715,7 @@ int gemma_kv_pages_compact(const gemma_page_book* book, const gemma_page_pool* p
   plan.copies = take(3 * n_pages);
   if (page_map) plan.map = page_map;
   const int smem = (book->n_pages + 31) / 32 * 4;
-  cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024) e = cudaFuncSetAttribute(k_pages_compact, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_shared(k_pages_compact, MAX_PAGES / 8);
   if (e != cudaSuccess) return cuda_err(e, "page compact");
   k_pages_compact<<<1, PLAN_T, smem, st>>>(book_of(book), plan, n_live);
   e = cudaGetLastError();

@@ -439,7 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
     unsigned char* sO = sm;  // Q buffer
     if (ok) {
       tc::fence_after_sync();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = SK || l > 0.f ? 1.f / l : 0.f;  // SK: as in prefill_stream.cu, 0 and NaN are to show
 #pragma unroll 1
       for (int c = 0; c < 8; ++c) {
         uint32_t o[32];
@@ -459,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
       }
       if (row_valid && a.lse && vh == 0)
         a.lse[((int64_t)b * a.Hq + h) * a.S + q0 + row] =
-            l > 0.f ? (m_used + __log2f(l)) * 0.69314718055994530942f : -INFINITY;
+            SK || l > 0.f ? (m_used + __log2f(l)) * 0.69314718055994530942f : -INFINITY;
     }
     fence_proxy_async_smem();
     asm volatile("bar.sync 1, 128;" ::: "memory");  // the four softmax warps

@@ -351,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(STREAM_T, 1)
     int out_b = 0, out_h = 0, out_q0 = 0;
     const auto put_out = [&]() {
       tc::fence_after_sync();
-      const float inv = out_l > 0.f ? 1.f / out_l : 0.f;
+      const float inv = 1.f / out_l;  // a row sees a key, itself: 0 (logits of -inf) and NaN are to show
 #pragma unroll 1
       for (int c = half * 2; c < half * 2 + 2; ++c) {
         uint32_t o[2][32];
@@ -391,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(STREAM_T, 1)
       }
       if (half == 0 && out_q0 + row < a.S && a.lse)
         a.lse[((int64_t)out_b * a.Hq + out_h) * a.S + out_q0 + row] =
-            out_l > 0.f ? (out_m + __log2f(out_l)) * 0.69314718055994530942f : -INFINITY;
+            (out_m + __log2f(out_l)) * 0.69314718055994530942f;
     };
     uint64_t deadline = 0;
     // P V of the key tile before the current one is complete (all earlier ones are

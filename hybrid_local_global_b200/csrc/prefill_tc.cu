@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(192, 1)
       }
     } else if (ok) {
       tc::fence_after_sync();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = SK || l > 0.f ? 1.f / l : 0.f;  // SK: as in prefill_stream.cu, 0 and NaN are to show
 #pragma unroll 1
       for (int c = 0; c < 8; ++c) {
         uint32_t o[32];
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(192, 1)
       }
       if (row_valid && a.lse && vh == 0)
         a.lse[((int64_t)b * a.Hq + h) * a.S + q0 + row] =
-            l > 0.f ? (m_used + __log2f(l)) * 0.69314718055994530942f : -INFINITY;
+            SK || l > 0.f ? (m_used + __log2f(l)) * 0.69314718055994530942f : -INFINITY;
     }
     fence_proxy_async_smem();
     asm volatile("bar.sync 1, 128;" ::: "memory");  // the four softmax warps
@@ -716,14 +716,13 @@ __global__ void __launch_bounds__(192, 1)
         v[r].x = v[r].x == -INFINITY ? 0.f : tc::ex2(v[r].x - M);  // no visible key there
         L += v[r].x * v[r].y;
       }
-      const float inv = L > 0.f ? 1.f / L : L;  // NaN stays NaN
+      const float inv = 1.f / L;  // NaN stays NaN, and so does 0 / 0 (every logit -inf)
 #pragma unroll
       for (int r = 0; r < 8; ++r) wgt[row * 12 + r] = v[r].x * inv;
       wgt[row * 12 + 8] = bad;
       const int t = t0 + row / G;
       if (a.lse && vh == 0 && own == 0 && row < G * a.tokens && t < a.S && bad == 0.f)
-        a.lse[((int64_t)b * a.Hq + g * G + row % G) * a.S + t] =
-            L > 0.f ? (M + __log2f(L)) * 0.69314718055994530942f : -INFINITY;
+        a.lse[((int64_t)b * a.Hq + g * G + row % G) * a.S + t] = (M + __log2f(L)) * 0.69314718055994530942f;
     }
     __syncthreads();
     const int groups = cols / 8;  // 16 bytes of output

@@ -96,3 +96,79 @@ def test_decode_keys(case, rows):
     hit = torch.zeros(B, Hq, dtype=torch.bool, device=DEV)
     hit[b, g * (Hq // Hkv):(g + 1) * (Hq // Hkv)] = any(j >= n - window for j in spots)  # some key that is seen
     check(run(q, [k, pools[1]]), clean, hit)
+
+
+# before, new tokens, window, q heads, KV heads, dim: a chunk split over a cluster, pairs that walk row
+# tiles, head pairs, one head per CTA
+PREFILL = [([300], 40, 700, 8, 1, 512), ([200, 31], 20, 90, 4, 1, 256), ([513, 100], 200, 128, 16, 16, 256),
+           ([300, 17], 130, 150, 16, 8, 512), ([0, 260], 129, 70, 8, 8, 512)]
+
+
+def prefill_setup(before, S, window, Hq, Hkv, D):
+    B, pps = len(before), (max(before) + S) // 128 + 1
+    pools, table = cache(B, pps, Hkv, D, S)
+    gen = synth.generator(S + D)
+    q, k, v = (synth.randn_bf16((B, S, h, D), gen).to(DEV) for h in (Hq, Hkv, Hkv))
+    lens = torch.tensor(before, dtype=torch.int32, device=DEV)
+
+    def run(q, k=k, pools=pools):
+        out = torch.full_like(q, 7.0)
+        lse = torch.full((B, Hq, S), 7.0, dtype=torch.float32, device=DEV)
+        native.gemma_attn_prefill_sinks(q, k, v, *[p.clone() for p in pools], table, window=window, sinks=5,
+                                        scale=D ** -0.5, out=out, lse=lse, seq_lens_before=lens, **KW)
+        assert native.gemma_attn_sync_status() == 0
+        return out, lse.transpose(1, 2)
+
+    return q, k, pools, table, run
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf], ids=str)
+@pytest.mark.parametrize("case", PREFILL, ids=str)
+def test_prefill_query(case, bad):
+    before, S, _, Hq, _, D = case
+    q, _, _, _, run = prefill_setup(*case)
+    clean, clean_lse = run(q)
+    x, hit = q.clone(), torch.zeros(len(before), S, Hq, dtype=torch.bool, device=DEV)
+    for b, s, h in ((0, 0, 0), (0, 7, Hq - 1), (len(before) - 1, S - 1, Hq // 2)):
+        x[b, s, h, D - 1] = bad
+        hit[b, s, h] = True
+    out, lse = run(x)
+    check(out, clean, hit)
+    assert torch.equal(lse[~hit], clean_lse[~hit])
+    if math.isnan(bad):
+        assert torch.isnan(lse[hit]).all(), lse[hit]
+
+
+@pytest.mark.parametrize("case", PREFILL, ids=str)
+def test_prefill_logits_all_minus_infinity(case):
+    """0 / 0: the only key that the first token sees has a logit of -inf."""
+    before, S, _, Hq, Hkv, D = case
+    case = ([0] * len(before), S, 1, Hq, Hkv, D)
+    q, k, _, _, run = prefill_setup(*case)
+    k = k.clone()
+    k[0, 0, :, D - 1] = 1.0
+    clean, _ = run(q, k)
+    x, hit = q.clone(), torch.zeros(len(before), S, Hq, dtype=torch.bool, device=DEV)
+    x[0, 0, 1, D - 1] = -math.inf
+    hit[0, 0, 1] = True
+    out, lse = run(x, k)
+    check(out, clean, hit)
+    assert lse[0, 0, 1] == -math.inf
+
+
+@pytest.mark.parametrize("case", PREFILL, ids=str)
+def test_prefill_keys(case):
+    """A cached key that is NaN reaches the tokens that see it, and no other."""
+    before, S, window, Hq, Hkv, D = case
+    q, _, pools, table, run = prefill_setup(*case)
+    clean, clean_lse = run(q)
+    b = max(range(len(before)), key=lambda i: before[i])
+    j, g = before[b] - 3, Hkv - 1
+    k = pools[0].clone()
+    k[table[b, j // 128], g, j % 128, 9] = math.nan
+    hit = torch.zeros(len(before), S, Hq, dtype=torch.bool, device=DEV)
+    seen = [s for s in range(S) if j > before[b] + s - window]
+    hit[b, seen, g * (Hq // Hkv):(g + 1) * (Hq // Hkv)] = True
+    out, lse = run(q, pools=[k, pools[1]])
+    check(out, clean, hit)
+    assert torch.isnan(lse[hit]).all() and torch.equal(lse[~hit], clean_lse[~hit])

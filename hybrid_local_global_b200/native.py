@@ -152,6 +152,18 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _scratch(n, device, stream):
+    """A workspace of n bytes for a call on `stream` (None: the current one).
+    Allocated on that stream: the allocator hands the memory on in the order of
+    the stream it was allocated on, so that neither what ran there before nor
+    what the block serves next, once the call has returned, overlaps the call's
+    kernels."""
+    if stream is None:
+        return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(n, 1), dtype=torch.uint8, device=device)
+
+
 def _bf16(t, name):
     if t is None or isinstance(t, Int8KVCache):
         return
@@ -186,7 +198,7 @@ def gemma_attn_prefill(q, k_new, v_new, k_cache, v_cache, *, window, rope_frac, 
         n = (gemma_attn_prefill_workspace_size_cached(B, S, Hq, Hkv, D, window, cap, flags)
              if seq_lens_before is not None or flags & GEMMA_F_SHARED
              else gemma_attn_prefill_workspace_size(B, S, Hq, Hkv, D, window))
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(n, q.device, stream)
     return _check(_prefill(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), cap,
                            _ptr(seq_lens_before), B, S, window, Hq, Hkv, D, rope_frac, rope_theta,
                            scale, _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), flags,
@@ -211,7 +223,7 @@ def gemma_attn_decode(q, k_new, v_new, k_cache, v_cache, *, seq_lens, max_seq_le
     flags |= _kv_kind(k_cache, v_cache)
     if workspace is None:
         n = gemma_attn_decode_workspace_size(B, Hq, Hkv, D, window, max_seq_len)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(n, q.device, stream)
     return _check(_decode(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), cap,
                           _ptr(seq_lens), max_seq_len, B, window, Hq, Hkv, D, rope_frac,
                           rope_theta, scale, _ptr(out), _ptr(workspace), workspace.numel(), flags,
@@ -237,7 +249,7 @@ def gemma_attn_decode_multi(q, k_new, v_new, k_cache, v_cache, *, seq_lens, max_
     flags |= _kv_kind(k_cache, v_cache)
     if workspace is None:
         n = gemma_attn_decode_multi_workspace_size(B, T, Hq, Hkv, D, window, max_seq_len, cap, flags)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(n, q.device, stream)
     return _check(_multi(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), cap,
                          _ptr(seq_lens), max_seq_len, B, T, window, Hq, Hkv, D, rope_frac,
                          rope_theta, scale, _ptr(out), _ptr(workspace), workspace.numel(), flags,
@@ -266,7 +278,7 @@ def gemma_attn_prefill_paged(q, k_new, v_new, k_pool, v_pool, page_table, *, rop
         n = (gemma_attn_prefill_workspace_size_cached(B, S, Hq, Hkv, D, 0, ps * pps, flags)
              if seq_lens_before is not None or flags & GEMMA_F_SHARED
              else gemma_attn_prefill_workspace_size(B, S, Hq, Hkv, D, 0))
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(n, q.device, stream)
     return _check(_prefill_paged(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool), _ptr(v_pool), _ptr(page_table),
                                  ps, pps, n_pages, _ptr(seq_lens_before), B, S, Hq, Hkv, D, rope_frac, rope_theta,
                                  scale, _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), flags,
@@ -286,7 +298,7 @@ def gemma_attn_decode_paged(q, k_new, v_new, k_pool, v_pool, page_table, *, seq_
     flags |= _kv_kind(k_pool, v_pool)
     if workspace is None:
         n = gemma_attn_decode_workspace_size(B, Hq, Hkv, D, 0, max_seq_len)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(n, q.device, stream)
     return _check(_decode_paged(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool), _ptr(v_pool), _ptr(page_table),
                                 ps, pps, n_pages, _ptr(seq_lens), max_seq_len, B, Hq, Hkv, D, rope_frac,
                                 rope_theta, scale, _ptr(out), _ptr(workspace), workspace.numel(), flags,
@@ -307,7 +319,7 @@ def gemma_attn_decode_multi_paged(q, k_new, v_new, k_pool, v_pool, page_table, *
     flags |= _kv_kind(k_pool, v_pool)
     if workspace is None:
         n = gemma_attn_decode_multi_workspace_size(B, T, Hq, Hkv, D, 0, max_seq_len, ps * pps, flags)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(n, q.device, stream)
     return _check(_multi_paged(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pool), _ptr(v_pool), _ptr(page_table),
                                ps, pps, n_pages, _ptr(seq_lens), max_seq_len, B, T, Hq, Hkv, D, rope_frac,
                                rope_theta, scale, _ptr(out), _ptr(workspace), workspace.numel(), flags,
@@ -503,13 +515,13 @@ def _sinks_args(q, k_new, v_new, k_pool, v_pool, page_table, out, lens, lens_nam
     return i, args, (B, Hq, Hkv, D), _need(out, "out", _BF16, qs, i), flags
 
 
-def _workspace(workspace, size, index):
-    """(pointer, bytes) of the caller's workspace, or of one of size() bytes."""
+def _workspace(workspace, size, index, stream):
+    """(tensor, pointer, bytes) of the caller's workspace, or of one of size() bytes."""
     if workspace is None:
         n = size()
         if n == 0:
             return None, None, 0
-        workspace = torch.empty(n, dtype=torch.uint8, device="cuda:%d" % index)
+        workspace = _scratch(n, "cuda:%d" % index, stream)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous tensor on device %d" % index)
     return workspace, workspace.data_ptr(), workspace.nbytes
@@ -525,7 +537,7 @@ def gemma_attn_prefill_sinks(q, k_new, v_new, k_pool, v_pool, page_table, *, win
                                                          seq_lens_before, "seq_lens_before", flags)
     S = q.shape[1]
     lse_p = None if lse is None else _need(lse, "lse", torch.float32, (B, Hq, S), i)
-    keep, ws, ws_bytes = _workspace(workspace, lambda: gemma_attn_prefill_workspace_size(B, S, Hq, Hkv, D, 0), i)
+    keep, ws, ws_bytes = _workspace(workspace, lambda: gemma_attn_prefill_workspace_size(B, S, Hq, Hkv, D, 0), i, stream)
     return _on(i, stream, "gemma_attn_prefill_sinks", _prefill_sinks, *args, B, S, window, sinks, Hq, Hkv, D, rope_frac,
                rope_theta, scale, out_p, lse_p, ws, ws_bytes, flags)
 
@@ -546,7 +558,7 @@ def gemma_attn_decode_sinks(q, k_new, v_new, k_pool, v_pool, page_table, *, seq_
     i, args, (B, Hq, Hkv, D), out_p, flags = _sinks_args(q, k_new, v_new, k_pool, v_pool, page_table, out, seq_lens,
                                                          "seq_lens", flags)
     keep, ws, ws_bytes = _workspace(
-        workspace, lambda: gemma_attn_decode_sinks_workspace_size(B, Hq, Hkv, D, window, sinks, max_seq_len), i)
+        workspace, lambda: gemma_attn_decode_sinks_workspace_size(B, Hq, Hkv, D, window, sinks, max_seq_len), i, stream)
     return _on(i, stream, "gemma_attn_decode_sinks", _decode_sinks, *args, max_seq_len, B, window, sinks, Hq, Hkv, D,
                rope_frac, rope_theta, scale, out_p, ws, ws_bytes, flags)
 
@@ -599,9 +611,9 @@ def gemma_kv_pages_fork(book, parents, *, stream=None):
                _need(parents, "parents", _I32, (book.n_seqs,), i))
 
 
-def _book_workspace(book, workspace):
-    return _workspace(workspace,
-                      lambda: gemma_kv_pages_workspace_size(book.n_seqs, book.pages_per_seq, book.n_pages), book._index)
+def _book_workspace(book, workspace, stream):
+    return _workspace(workspace, lambda: gemma_kv_pages_workspace_size(book.n_seqs, book.pages_per_seq, book.n_pages),
+                      book._index, stream)
 
 
 def gemma_kv_pages_reserve(book, pools, *, seq_lens, new_tokens, lacking, workspace=None, stream=None):
@@ -612,7 +624,7 @@ def gemma_kv_pages_reserve(book, pools, *, seq_lens, new_tokens, lacking, worksp
     lens, new = _need(seq_lens, "seq_lens", _I32, n, i), _need(new_tokens, "new_tokens", _I32, n, i)
     short = _need(lacking, "lacking", _I32, (1,), i)
     arr = _pool_list(pools, book.n_pages, book.page_size, i)
-    keep, ws, ws_bytes = _book_workspace(book, workspace)
+    keep, ws, ws_bytes = _book_workspace(book, workspace, stream)
     return _on(i, stream, "gemma_kv_pages_reserve", _pages_reserve, book._ref, arr, len(pools), lens, new, short, ws,
                ws_bytes)
 
@@ -632,7 +644,7 @@ def gemma_kv_pages_compact(book, pools, *, n_live, page_map=None, workspace=None
     live = _need(n_live, "n_live", _I32, (1,), i)
     names = None if page_map is None else _need(page_map, "page_map", _I32, (book.n_pages,), i)
     arr = _pool_list(pools, book.n_pages, book.page_size, i)
-    keep, ws, ws_bytes = _book_workspace(book, workspace)
+    keep, ws, ws_bytes = _book_workspace(book, workspace, stream)
     return _on(i, stream, "gemma_kv_pages_compact", _pages_compact, book._ref, arr, len(pools), live, names, ws, ws_bytes)
 
 

@@ -120,15 +120,17 @@ class AttentionStack:
             return self.descs[l].shared_from
         return l if self._has_sharers(l) else None
 
-    def _window_workspace(self, src: int, nbytes: int):
+    def _window_workspace(self, src: int, nbytes: int, stream=None):
         """The workspace a source layer and its sharers use for one chunk
-        (kept per source: layers in between must not write it)."""
+        (kept per source: layers in between must not write it), for calls on
+        `stream` (None: the current one)."""
         if not hasattr(self, "_win_ws"):
             self._win_ws = {}
         buf = self._win_ws.get(src)
         if buf is None or buf.numel() < nbytes:
-            buf = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=self.device)
-            self._win_ws[src] = buf
+            buf = self._win_ws[src] = native._scratch(nbytes, self.device, stream)
+        if buf.is_cuda:  # a larger one may take its place while this call runs
+            buf.record_stream(stream or torch.cuda.current_stream(buf.device))
         return buf
 
     def prefill_layer(self, l: int, q, k, v, out, *, workspace, seq_lens_before=None, lse=None,
@@ -145,7 +147,7 @@ class AttentionStack:
             n = native.gemma_attn_prefill_workspace_size_cached(
                 q.shape[0], q.shape[1], q.shape[2], t.n_kv_heads, t.head_dim, t.window, t.window,
                 native.GEMMA_F_KV_INT8 if self.w.kv_int8 else 0)
-            workspace = self._window_workspace(src, n)
+            workspace = self._window_workspace(src, n, stream)
         native.gemma_attn_prefill(
             q, None if shared else k, None if (shared or keqv) else v, self.k_cache[l],
             None if keqv else self.v_cache[l],
@@ -237,7 +239,7 @@ class AttentionStack:
             n = native.gemma_attn_decode_multi_workspace_size(
                 q.shape[0], q.shape[1], q.shape[2], t.n_kv_heads, t.head_dim, t.window, max_seq_len, t.window,
                 flags | (native.GEMMA_F_KV_INT8 if self.w.kv_int8 else 0))
-            workspace = self._window_workspace(src, n)
+            workspace = self._window_workspace(src, n, stream)
         native.gemma_attn_decode_multi(
             q, None if shared else k, None if (shared or keqv) else v, self.k_cache[l],
             None if keqv else self.v_cache[l],

@@ -105,19 +105,54 @@ int err(int code, const char* msg) { return record_error(code, msg); }
 
 // Strided vectors [tokens][heads][D]: 16-byte loads need every token to start
 // on 16 bytes; a token's heads are dense.
-int check_side(const void* p, long long stride, const void* out, long long out_stride, int tokens, int heads, int D) {
-  if (!p || !out) return err(GEMMA_ERR_INVALID_ARG, "null tensor pointer");
-  if ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(out)) & 15u || (stride | out_stride) % 8)
+struct Side {
+  const void* p;
+  long long stride, row;  // elements between tokens, and of a token
+};
+
+int check_side(const Side& s, int tokens) {
+  if (!s.p) return err(GEMMA_ERR_INVALID_ARG, "null tensor pointer");
+  if (reinterpret_cast<uintptr_t>(s.p) & 15u || s.stride % 8)
     return err(GEMMA_ERR_INVALID_ARG, "tensors must be 16-byte aligned with token strides of a multiple of 8 elements");
-  const long long row = (long long)heads * D;
-  if (tokens > 1 && (stride < row || out_stride < row))
+  if (tokens > 1 && s.stride < s.row)
     return err(GEMMA_ERR_INVALID_ARG, "a token stride is smaller than heads * head_dim");
-  // in place, or apart
-  const char* a = static_cast<const char*>(p);
-  const char* b = static_cast<const char*>(out);
-  const long long na = ((tokens - 1) * stride + row) * 2, nb = ((tokens - 1) * out_stride + row) * 2;
-  if (a == b ? (tokens > 1 && stride != out_stride) : (a < b + nb && b < a + na))
+  if (tokens > 1 && s.stride > (1LL << 60) / tokens) return err(GEMMA_ERR_INVALID_ARG, "token stride out of range");
+  return GEMMA_OK;
+}
+
+// Whether some token of one tensor shares bytes with some token of the other.
+// With one stride: token i of a and token j of b do iff, for t = i - j,
+//   d - a.row < t * stride < d + b.row   (d: elements from a to b),
+// so head slices of one buffer, interleaved as they are, do not. Tensors of
+// different strides are told apart by their extents alone.
+bool overlap(const Side& a, const Side& b, int tokens) {
+  const long long n = tokens - 1;
+  // both 16-byte aligned
+  const long long d = (long long)(reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p)) / 2;
+  if (d >= n * a.stride + a.row || -d >= n * b.stride + b.row) return false;
+  if (n == 0 || a.stride != b.stride) return true;
+  const auto floor_div = [](long long x, long long y) { return x / y - (x % y < 0); };
+  const long long first = floor_div(d - a.row, a.stride) + 1, last = floor_div(d + b.row - 1, a.stride);
+  return std::max(first, -n) <= std::min(last, n);
+}
+
+// q into q_out and, if any, k into k_out. A thread reads a vector before it
+// writes it, so an output may be its input; any other sharing would let one
+// token's output go under another's input.
+int check_tensors(const Side& q, const Side& q_out, const Side& k, const Side& k_out, int tokens, bool has_k) {
+  int rc = check_side(q, tokens);
+  if (!rc) rc = check_side(q_out, tokens);
+  if (!rc && has_k) rc = check_side(k, tokens);
+  if (!rc && has_k) rc = check_side(k_out, tokens);
+  if (rc) return rc;
+  const auto clash = [tokens](const Side& in, const Side& out) {
+    const bool same = in.p == out.p && (tokens == 1 || in.stride == out.stride);
+    return !same && overlap(in, out, tokens);
+  };
+  if (clash(q, q_out) || (has_k && clash(k, k_out)))
     return err(GEMMA_ERR_INVALID_ARG, "an output must be its input (same stride) or must not overlap it");
+  if (has_k && (overlap(q_out, k, tokens) || overlap(k_out, q, tokens) || overlap(q_out, k_out, tokens)))
+    return err(GEMMA_ERR_INVALID_ARG, "an output overlaps the other input or output");
   return GEMMA_OK;
 }
 
@@ -150,8 +185,9 @@ extern "C" int gemma_rope_axes(const void* q, long long q_stride, const void* k,
   if (tokens == 0) return record_ok();
   if (!positions || reinterpret_cast<uintptr_t>(positions) & 3u)
     return err(GEMMA_ERR_INVALID_ARG, "positions: null or misaligned pointer");
-  int rc = check_side(q, q_stride, q_out, q_out_stride, tokens, n_q_heads, head_dim);
-  if (!rc && n_kv_heads) rc = check_side(k, k_stride, k_out, k_out_stride, tokens, n_kv_heads, head_dim);
+  const long long q_row = (long long)n_q_heads * head_dim, k_row = (long long)n_kv_heads * head_dim;
+  const int rc = check_tensors(Side{q, q_stride, q_row}, Side{q_out, q_out_stride, q_row}, Side{k, k_stride, k_row},
+                               Side{k_out, k_out_stride, k_row}, tokens, n_kv_heads > 0);
   if (rc) return rc;
 
   AxesArgs a;

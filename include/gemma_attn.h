@@ -455,8 +455,12 @@ int gemma_kv_pages_copy(const gemma_page_pool* pools, int n_pools, int n_pages, 
 /*        turn with each axis, in all at most head_dim / 2; the remaining    */
 /*        pairs (the last ones) are copied.                                  */
 /* Pair i turns by positions[axis][t] * rope_theta^(-2i/head_dim).            */
-/* Outputs: written with strides of their own; an output is its input (same */
-/*        pointer and stride) or does not overlap it, nor the other one.     */
+/* Outputs: written with strides of their own. An output is its own input   */
+/*        (same pointer and stride) or shares no bytes with it, nor with the */
+/*        other input, nor with the other output (else                       */
+/*        GEMMA_ERR_INVALID_ARG). Other head slices of the same buffer with  */
+/*        the same stride will do; tensors with different strides must not   */
+/*        lie within one another's extent.                                   */
 /* flags:                                                                   */
 /*   GEMMA_ROPE_INTERLEAVED: pairs go to the axes in turn (while an axis     */
 /*        has pairs left); without it the first axis_pairs[0] pairs belong   */

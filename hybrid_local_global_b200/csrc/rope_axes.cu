@@ -227,7 +227,7 @@ extern "C" int gemma_rope_axes(const void* q, long long q_stride, const void* k,
   a.Hq = n_q_heads;
   a.Hkv = n_kv_heads;
   a.D = head_dim;
-  const int per_cta = AX_T / (head_dim / 8), ctas = (tokens + per_cta - 1) / per_cta;
+  const int per_cta = AX_T / (head_dim / 8), ctas = (tokens - 1) / per_cta + 1;  // tokens may be the largest int
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (ctas >= multiprocessors()) {
     k_rope_axes<8><<<ctas, AX_T, 0, st>>>(a);

@@ -477,6 +477,14 @@ def _on(index, stream, what, call, *args):
         return _check(call(*args, raw))
 
 
+def _int32(**numbers):
+    """Refuses numbers that a C int would not hold (ctypes keeps their low 32
+    bits without a word)."""
+    for name, x in numbers.items():
+        if not -2 ** 31 <= x < 2 ** 31:
+            raise ValueError("%s %d does not fit in 32 bits" % (name, x))
+
+
 def _need(t, name, dtype, shape, index):
     """The data pointer of a contiguous tensor of this type, shape and device."""
     if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
@@ -533,6 +541,7 @@ def gemma_attn_prefill_sinks(q, k_new, v_new, k_pool, v_pool, page_table, *, win
     first `sinks`: tensors as gemma_attn_prefill_paged (bf16 pools)."""
     if q.dim() != 4:
         raise ValueError("q must be [B, S, Hq, D]")
+    _int32(window=window, sinks=sinks)
     i, args, (B, Hq, Hkv, D), out_p, flags = _sinks_args(q, k_new, v_new, k_pool, v_pool, page_table, out,
                                                          seq_lens_before, "seq_lens_before", flags)
     S = q.shape[1]
@@ -555,6 +564,7 @@ def gemma_attn_decode_sinks(q, k_new, v_new, k_pool, v_pool, page_table, *, seq_
         raise TypeError("seq_lens is required")
     if q.dim() != 3:
         raise ValueError("q must be [B, Hq, D]")
+    _int32(window=window, sinks=sinks, max_seq_len=max_seq_len)
     i, args, (B, Hq, Hkv, D), out_p, flags = _sinks_args(q, k_new, v_new, k_pool, v_pool, page_table, out, seq_lens,
                                                          "seq_lens", flags)
     keep, ws, ws_bytes = _workspace(
@@ -632,6 +642,7 @@ def gemma_kv_pages_reserve(book, pools, *, seq_lens, new_tokens, lacking, worksp
 def gemma_kv_pages_trim(book, *, seq_lens, window=0, sinks=0, stream=None):
     """Drops the pages that hold nothing a token after seq_lens[b] sees
     (int32 [n_seqs]; 0 ends the sequence, below 0 leaves its row alone)."""
+    _int32(window=window, sinks=sinks)
     i = book._index
     return _on(i, stream, "gemma_kv_pages_trim", _pages_trim, book._ref,
                _need(seq_lens, "seq_lens", _I32, (book.n_seqs,), i), window, sinks)
@@ -705,8 +716,9 @@ def gemma_rope_axes(q, k, positions, *, axis_pairs, rope_theta, q_out, k_out=Non
             raise ValueError("k_out must have the shape of k")
         ks, kos = _token_stride(k, "k", i), _token_stride(k_out, "k_out", i)
         k_p, ko_p = k.data_ptr(), k_out.data_ptr()
-    n_axes = len(axis_pairs)
+    n_axes, tokens = len(axis_pairs), math.prod(lead)
+    _int32(tokens=tokens)
     pos = _need(positions, "positions", _I32, (n_axes, *lead), i)
     return _on(i, stream, "gemma_rope_axes", _rope_axes, q.data_ptr(), qs, k_p, ks, pos, n_axes,
-               (_I * max(n_axes, 1))(*axis_pairs), math.prod(lead), Hq, Hkv, D, rope_theta, q_out.data_ptr(), qos, ko_p,
+               (_I * max(n_axes, 1))(*axis_pairs), tokens, Hq, Hkv, D, rope_theta, q_out.data_ptr(), qos, ko_p,
                kos, flags)

@@ -474,6 +474,10 @@ int cuda_err(cudaError_t e, const char* what) {
 
 bool misaligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
+bool within_limits(int n_seqs, int pages_per_seq, int n_pages) {
+  return n_seqs <= MAX_SEQS && n_pages <= MAX_PAGES && (int64_t)n_seqs * pages_per_seq <= (1 << 30);
+}
+
 int check_book(const gemma_page_book* b) {
   if (!b || !b->page_table || !b->ref_count) return err(GEMMA_ERR_INVALID_ARG, "page book: null pointer");
   if (b->n_seqs <= 0 || b->pages_per_seq <= 0 || b->n_pages <= 0)
@@ -482,7 +486,7 @@ int check_book(const gemma_page_book* b) {
     return err(GEMMA_ERR_INVALID_ARG, "page book: page_size must be a positive multiple of 128");
   if ((int64_t)b->pages_per_seq * b->page_size > INT32_MAX)
     return err(GEMMA_ERR_INVALID_ARG, "page book: pages_per_seq * page_size exceeds 2^31");
-  if (b->n_seqs > MAX_SEQS || b->n_pages > MAX_PAGES || (int64_t)b->n_seqs * b->pages_per_seq > (1 << 30))
+  if (!within_limits(b->n_seqs, b->pages_per_seq, b->n_pages))
     return err(GEMMA_ERR_UNSUPPORTED, "page book: more than 4096 rows, 2^20 pages or 2^30 table entries");
   if (misaligned(b->page_table, 4) || misaligned(b->ref_count, 4))
     return err(GEMMA_ERR_INVALID_ARG, "page book: misaligned pointer");
@@ -594,7 +598,7 @@ using namespace hlg;
 extern "C" {
 
 size_t gemma_kv_pages_workspace_size(int n_seqs, int pages_per_seq, int n_pages) {
-  if (n_seqs <= 0 || pages_per_seq <= 0 || n_pages <= 0) return 0;
+  if (n_seqs <= 0 || pages_per_seq <= 0 || n_pages <= 0 || !within_limits(n_seqs, pages_per_seq, n_pages)) return 0;
   return plan_bytes(n_seqs, pages_per_seq, n_pages);
 }
 

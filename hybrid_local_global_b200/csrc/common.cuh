@@ -212,12 +212,6 @@ __device__ __forceinline__ bool mbar_wait_bounded_at(uint64_t* bar, uint32_t par
   return true;
 }
 
-__device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity,
-                                                  volatile int* abort_flag,
-                                                  uint64_t deadline_ns, int* status) {
-  return mbar_wait_bounded_at(bar, parity, abort_flag, deadline_ns, status, -1, 0, 0, 0);
-}
-
 // 1-D bulk copy global -> shared, completion signalled as tx bytes on `bar`.
 __device__ __forceinline__ void bulk_g2s(void* smem_dst, const void* gmem_src, uint32_t bytes,
                                          uint64_t* bar) {

@@ -21,7 +21,7 @@
 //               held one 512-byte row per copy (head_dim 256) to half the HBM
 //               rate; 2 KB copies (4 rows at head_dim 256, 2 at 512) lift
 //               that. The MMA fragments take the keys of a sub-block in an
-//               order (ring_key) that spreads each ldmatrix over row groups.
+//               order (key_of) that spreads each ldmatrix over row groups.
 //   warps 0..2  consumers: sub-block t goes to warp t % 3 and ring slot
 //               t % NSLOT, with NSLOT a multiple of 3, so every slot has a
 //               single consumer that waits its phases strictly in order
@@ -43,7 +43,6 @@
 #include <algorithm>
 
 #include "common.cuh"
-#include "decode_ring.cuh"
 #include "kernels.h"
 #include "mma_sync.cuh"
 
@@ -61,7 +60,7 @@ struct DecCfg {
   static constexpr int ROW = D + 8;             // padded smem row of Q (elements)
   static constexpr int ROWB = ROW * 2;          // bytes
   static constexpr int RPC = RPC_;                 // rows per bulk copy
-  static constexpr int GROUPB = ring_group_bytes(D, RPC);  // RPC consecutive K (or V) rows + 16 B pad
+  static constexpr int GROUPB = RPC * D * 2 + 16;  // RPC consecutive K (or V) rows + 16 B pad
   static constexpr int GPR = KB / RPC;             // row groups per 16-row region
   static constexpr int SLOT_B = 2 * GPR * GROUPB;  // K region then V region (two K regions under K = V)
   static constexpr int NSLOT = 3;  // head_dim 256: with four CTAs per SM (see the launch bounds)
@@ -75,6 +74,24 @@ struct DecCfg {
   static constexpr int MISC_OFF = BAR_OFF + 2 * NSLOT * 8;
   static constexpr int SMEM = MISC_OFF + (1 + 2 * NSLOT + 64) * 4;
 };
+
+// byte offset of row r within a run of row groups
+template <int D, int RPC>
+__device__ __forceinline__ int group_row_off(int r) {
+  using C = DecCfg<D, RPC>;
+  return (r / C::RPC) * C::GROUPB + (r % C::RPC) * (D * 2);
+}
+
+// The key that MMA index n (0..15) of a 16-key sub-block stands for. S and
+// P.V only need the same order for the K and V fragments and the mask, so
+// the 8 rows each ldmatrix reads are taken from different row groups where
+// possible: rows of one group are D*2 bytes apart and share bank groups,
+// while consecutive groups are shifted by the 16-byte pad.
+template <int RPC>
+__device__ __forceinline__ int key_of(int n) {
+  constexpr int NG = 16 / RPC;  // row groups per 16 keys
+  return (n % NG) * RPC + n / NG;
+}
 
 // PAGED: the cache is a pool named by a.page_table (see cache_row); the
 // contiguous instance keeps the plain row arithmetic of one (b, g) range.
@@ -192,7 +209,7 @@ __global__ void __launch_bounds__(32 * (NCW + 1), D == 256 ? 4 : 2) k_decode_spl
     for (int mt = 0; mt < D / 16; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
     float m_h = -INFINITY, l_t = 0.f;
     const uint32_t q_addr = smem_u32(qs) + ((lane & 7) * C::ROW + ((lane >> 3) & 1) * 8) * 2;
-    const uint32_t frag_off = ring_row_off<D, RPC>(ring_key<RPC>((lane >> 4) * 8 + (lane & 7))) + ((lane >> 3) & 1) * 16;
+    const uint32_t frag_off = group_row_off<D, RPC>(key_of<RPC>((lane >> 4) * 8 + (lane & 7))) + ((lane >> 3) & 1) * 16;
 
     for (int t = warp; t < n_sub; t += NCW) {
       const int slot = t % C::NSLOT;
@@ -204,12 +221,12 @@ __global__ void __launch_bounds__(32 * (NCW + 1), D == 256 ? 4 : 2) k_decode_spl
       if (nk_slot < kps) {
         // rows past the end were not copied: make them finite zeros
         // (slot rows 0..15 are K, 16..31 V; under K = V all 32 are keys,
-        // and either way row r sits at ring_row_off(r))
+        // and either way row r sits at group_row_off(r))
         unsigned char* rows = ring + slot * C::SLOT_B;
         for (int idx = lane; idx < 2 * C::KB * (D / 8); idx += 32) {
           const int r = idx / (D / 8), c = (idx % (D / 8)) * 8;
           const int key = a.keqv ? r : (r & (C::KB - 1));
-          if (key >= nk_slot) *reinterpret_cast<uint4*>(rows + ring_row_off<D, RPC>(r) + c * 2) = make_uint4(0, 0, 0, 0);
+          if (key >= nk_slot) *reinterpret_cast<uint4*>(rows + group_row_off<D, RPC>(r) + c * 2) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -232,12 +249,12 @@ __global__ void __launch_bounds__(32 * (NCW + 1), D == 256 ? 4 : 2) k_decode_spl
         mma_bf16(s1, qa0, 0u, qa2, 0u, b2, b3);
       }
       // online softmax for head gq; this thread holds MMA columns 2tg, 2tg+1,
-      // 8+2tg, 9+2tg, i.e. keys ring_key() of those
+      // 8+2tg, 9+2tg, i.e. keys key_of() of those
       float sv[4];
-      sv[0] = (ring_key<RPC>(2 * tg) < nk) ? s0[0] * a.scale_log2 : -INFINITY;
-      sv[1] = (ring_key<RPC>(2 * tg + 1) < nk) ? s0[1] * a.scale_log2 : -INFINITY;
-      sv[2] = (ring_key<RPC>(8 + 2 * tg) < nk) ? s1[0] * a.scale_log2 : -INFINITY;
-      sv[3] = (ring_key<RPC>(9 + 2 * tg) < nk) ? s1[1] * a.scale_log2 : -INFINITY;
+      sv[0] = (key_of<RPC>(2 * tg) < nk) ? s0[0] * a.scale_log2 : -INFINITY;
+      sv[1] = (key_of<RPC>(2 * tg + 1) < nk) ? s0[1] * a.scale_log2 : -INFINITY;
+      sv[2] = (key_of<RPC>(8 + 2 * tg) < nk) ? s1[0] * a.scale_log2 : -INFINITY;
+      sv[3] = (key_of<RPC>(9 + 2 * tg) < nk) ? s1[1] * a.scale_log2 : -INFINITY;
       float tmax = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3]));
       tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
       tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 2));
@@ -423,7 +440,7 @@ cudaError_t launch_split(const DecodeAttnArgs& a, int B, cudaStream_t st) {
 
 }  // namespace
 
-// Rows per bulk copy (measured on B200, with ring_key's fragment order):
+// Rows per bulk copy (measured on B200, with key_of's fragment order):
 // head_dim 256 copies groups of 4 rows (2 KB; the local layers of a
 // 64-sequence 31B batch: 348 us at one row per copy, 226 at pairs, 185 at 4,
 // 205 at 8 rows); head_dim 512 copies pairs (2 KB; that batch's global layer

@@ -70,18 +70,6 @@ __device__ __forceinline__ bool wait_bounded_cluster(uint64_t* bar, uint32_t par
   return true;
 }
 
-// 4-D tiled TMA load into this CTA's shared memory whose completion (tx
-// bytes) is signalled on an mbarrier of either CTA of the pair (`bar` is a
-// shared::cluster address, e.g. from map_to). No multicast.
-__device__ __forceinline__ void tma_load_4d_pair(uint32_t smem_dst, const void* tmap, int c0, int c1, int c2,
-                                                 int c3, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
-
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
@@ -101,38 +89,10 @@ __device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// ---------------------------------------------------------------- MMA (even CTA only)
-// D[tmem, both CTAs] (+)= A[smem, both] * B[smem, both]
-__device__ __forceinline__ void mma2_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
-}
-
-// D[tmem, both] (+)= A[tmem, both] * B[smem, both]
-__device__ __forceinline__ void mma2_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
-}
-
-// Arrive once on the mbarrier at `bar` (a shared::cta offset) in every CTA of
-// `cta_mask` when all tcgen05 ops issued so far by this thread are done.
-__device__ __forceinline__ void commit2_mc(uint32_t bar, uint16_t cta_mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          bar),
-      "h"(cta_mask)
-      : "memory");
-}
-
 // ---------------------------------------------------------------- warp-uniform issue (see tc.cuh)
+// 4-D tiled TMA load into this CTA's shared memory whose completion (tx
+// bytes) is signalled on an mbarrier of either CTA of the pair (`bar` is a
+// shared::cluster address, e.g. from map_to). No multicast.
 __device__ __forceinline__ void tma_load_4d_pair_if(uint32_t go, uint32_t smem_dst, const void* tmap, int c0, int c1,
                                                     int c2, int c3, uint32_t bar) {
   asm volatile(
@@ -143,6 +103,7 @@ __device__ __forceinline__ void tma_load_4d_pair_if(uint32_t go, uint32_t smem_d
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(go)
       : "memory");
 }
+// MMA (even CTA only): D[tmem, both CTAs] (+)= A[smem, both] * B[smem, both]
 __device__ __forceinline__ void mma2_ss_if(uint32_t go, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                            uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -152,6 +113,7 @@ __device__ __forceinline__ void mma2_ss_if(uint32_t go, uint32_t d_tmem, uint64_
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(go));
 }
+// D[tmem, both] (+)= A[tmem, both] * B[smem, both]
 __device__ __forceinline__ void mma2_ts_if(uint32_t go, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                            uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -161,6 +123,8 @@ __device__ __forceinline__ void mma2_ts_if(uint32_t go, uint32_t d_tmem, uint32_
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(go));
 }
+// Arrive once on the mbarrier at `bar` (a shared::cta offset) in every CTA of
+// `cta_mask` when all tcgen05 ops issued so far by the elected thread are done.
 __device__ __forceinline__ void commit2_mc_if(uint32_t go, uint32_t bar, uint16_t cta_mask) {
   asm volatile(
       "{\n\t.reg .pred e;\n\t"

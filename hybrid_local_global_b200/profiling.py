@@ -36,9 +36,10 @@ CSRC = os.path.join(os.path.dirname(os.path.abspath(__file__)), "csrc")
 
 # the sources each recorded kernel is built from
 KERNEL_SOURCES = {
-    "k_prefill_tc": ("prefill_tc.cu", "launch.h", "pair.cuh", "tc.cuh", "common.cuh", "tmap.cu", "tmap.h"),
-    "k_prefill_pair": ("prefill_pair.cu", "prefill_pair.cuh", "launch.h", "pair.cuh", "tc.cuh", "common.cuh", "tmap.cu", "tmap.h"),
-    "k_decode_split": ("decode.cu", "decode_ring.cuh", "mma_sync.cuh", "common.cuh"),
+    "k_prefill_tc": ("prefill_tc.cu", "prefill_row.cuh", "launch.h", "pair.cuh", "tc.cuh", "common.cuh", "tmap.cu", "tmap.h"),
+    "k_prefill_pair": ("prefill_pair.cu", "prefill_pair.cuh", "prefill_row.cuh", "launch.h", "pair.cuh", "tc.cuh",
+                       "common.cuh", "tmap.cu", "tmap.h"),
+    "k_decode_split": ("decode.cu", "mma_sync.cuh", "common.cuh"),
     "k_decode_split_q8": ("decode_q8.cu", "mma_sync.cuh", "tc.cuh", "common.cuh", "tmap.cu", "tmap.h"),
     "k_verify_tc": ("verify_tc.cu", "tc.cuh", "common.cuh", "tmap.cu", "tmap.h"),
 }

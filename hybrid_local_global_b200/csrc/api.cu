@@ -1136,6 +1136,11 @@ int gemma_attn_prefill_sinks(const void* q, const void* k_new, const void* v_new
   ra.Hkv = n_kv_heads;
   ra.n_rot = rope_rotated_pairs(head_dim, rope_frac);
   ra.log2_theta = std::log2((double)rope_theta);
+  // The MMAs take bf16: the queries are rounded once, after the rotation, and the
+  // weights P before P V (their sum is taken before). Together that is 0.0026 of the
+  // output's norm on the 8191-token local prompt, of which 0.0016 the output's own
+  // rounding; remainders in further MMA columns, as in decode, would double the
+  // products. So that no second rounding comes on top of it:
   // scale * log2(e) = +-2^e * c, 1 <= c < 2: the queries take the sign and the
   // power of two, which leave their bits alone, the attention kernel takes c
   // (tiny scales, whose power of two would take the queries below the normal
@@ -1180,7 +1185,10 @@ int gemma_attn_prefill_sinks(const void* q, const void* k_new, const void* v_new
   aa.pages_per_seq = pages_per_seq;
   aa.n_pages = n_pages;
   // head_dim 256, and 512 with an even number of q heads per KV head: pairs of
-  // heads (256 with an odd number: of row tiles)
+  // heads (256 with an odd number: of row tiles). 512 with an odd number: single
+  // CTAs. Only an even group was measured on all three, 32 heads on 4 for 2 x 4096
+  // tokens: head pairs 2588 us, pairs of row tiles 2677, single CTAs 3112; so the odd
+  // groups' choice is the one that is not measured to be the best.
   const bool even = (n_q_heads / n_kv_heads) % 2 == 0;
   {
     ProfScope p_attn(GEMMA_KERNEL_PREFILL_ATTN, st);

@@ -13,9 +13,11 @@
 // Two warps per 32 rows run the softmax, each with half the columns: with one,
 // a key tile took 3650 cycles, of which the softmax 2650; with two 2600, of
 // which 1024 are its exponentials at the special-function rate and the products
-// 2048. B1 S8191 Hq32 Hkv16, window 1024, 16 sinks: 355 us with one CTA per row
-// tile, 247 so (1390 TFLOP/s counting the masked parts of edge tiles), the
-// rotation before it another 97.
+// 2048. B1 S8191 Hq32 Hkv16, window 1024, 16 sinks, the whole call in bursts of 20
+// ms, which stay below the power limit (1965 MHz): 344 us (445 with one CTA per row
+// tile, before this kernel), 380 back to back for seconds (1680 MHz). By itself this
+// kernel takes 258 us (1240 TFLOP/s counting the masked parts of edge tiles; 283
+// at 1750 MHz) and the rotation 97; its start lies beside the rotation's end.
 //
 // Waits, timeouts and the clearing of V's unseen rows are k_prefill_pair's.
 #include <cuda.h>

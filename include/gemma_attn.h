@@ -332,7 +332,11 @@ int gemma_attn_decode_multi_paged(const void* q, const void* k_new, const void* 
 /*        nothing is written for it and it is no error. A length below 0 or */
 /*        above max_seq_len gives zeros and GEMMA_ERR_DEVICE_RANGE.          */
 /* Values at positions that no query of the call sees are not used, what-   */
-/* ever they hold.                                                          */
+/* ever they hold. A NaN or an infinity that a query sees shows in its out  */
+/* (and lse); in q or in a key it stays with the queries that see it. In a  */
+/* value it does so in decode only: prefill takes up to 256 queries at a    */
+/* time and gives those that do not see a key the weight 0, and 0 * NaN is  */
+/* NaN. So the tokens that pad a batch need finite values (any will do).    */
 /* flags: GEMMA_F_SHARED, GEMMA_F_KEQV. bf16 pools only (GEMMA_F_KV_INT8:   */
 /*        GEMMA_ERR_UNSUPPORTED). No two sequences of a call may write the  */
 /*        same page (gemma_kv_pages_reserve sees to that).                   */
@@ -436,7 +440,10 @@ int gemma_kv_pages_compact(const gemma_page_book* book, const gemma_page_pool* p
  * and counts are not involved. A pair is carried out iff both pages exist, no
  * other pair names the same destination, and no other pair with a different
  * source and destination writes its source; others are skipped and reported
- * (GEMMA_ERR_DEVICE_RANGE). src[i] == dst[i] copies nothing. */
+ * (GEMMA_ERR_DEVICE_RANGE). src[i] == dst[i] copies nothing. n_copies is at most
+ * n_pages. Each 16 KB that are copied compare their pair with the whole list, so
+ * a list is best kept to a few thousand pairs: beyond, that takes longer than the
+ * copy (several lists make several calls). */
 int gemma_kv_pages_copy(const gemma_page_pool* pools, int n_pools, int n_pages, int page_size,
                         const int32_t* src, const int32_t* dst, int n_copies, void* stream);
 
